@@ -11,6 +11,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -24,6 +25,7 @@ STATUS = {0: "DGF_OK", 1: "DGF_EINVAL", 2: "DGF_EUNSUPPORTED", 3: "DGF_EWORKSPAC
 
 # (name, restype, argtypes) of every exported entry point
 _P, _I64, _SZ, _I = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.c_int
+_F = ctypes.c_float
 SIGNATURES = {
     "dgf_abi_version": (_I, []),
     "dgf_leaf_size": (_I, []),
@@ -51,6 +53,19 @@ SIGNATURES = {
     "dgf_gemm_tree_typed": (_I, [_I, _P, _I64, _P, _I64, _P, _I64, _I64, _I64, _I64, _P, _SZ, _I, _P]),
     "dgf_act_fwd_typed": (_I, [_P, _P, _P, _I64, _I, _P]),
     "dgf_act_bwd_typed": (_I, [_P, _P, _P, _P, _P, _P, _I64, _I, _P]),
+    "dgf_norm_fwd": (_I, [_P, _I64, _P, _I64, _P, _P, _I64, _F, _P, _F, _P, _I64, _P, _I64, _P, _I64, _I64, _I, _P]),
+    "dgf_norm_bwd_workspace": (_SZ, [_I64, _I64]),
+    "dgf_norm_bwd": (_I, [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _P, _I64, _F, _P, _P, _P, _I64, _P, _I64,
+                          _P, _P, _I64, _P, _I64, _I64, _P, _SZ, _I, _P]),
+    "dgf_pack8": (_I, [_P, _I64, _P, _I64, _P, _I64, _I64, _I64, _I, _P]),
+    "dgf_unpack8": (_I, [_P, _I64, _P, _I64, _P, _I64, _I64, _I64, _I, _P]),
+    "dgf_act_bwd_q8": (_I, [_P, _I64, _P, _P, _P, _P, _I64, _I64, _P, _P, _P, _I64, _I64, _I64, _I, _P]),
+    "dgf_ffn_fwd_q8_workspace": (_SZ, [_I64, _I64, _I64]),
+    "dgf_ffn_fwd_q8": (_I, [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _P, _I64, _I64,
+                            _I64, _I64, _I64, _P, _SZ, _I, _P]),
+    "dgf_ffn_bwd_q8": (_I, [_P, _I64, _P, _I64, _P, _P, _P, _P, _I64, _I64, _P, _I64, _P, _I64, _P, _I64,
+                            _P, _P, _P, _I64, _P, _I64, _P, _I64, _P, _I64,
+                            _I64, _I64, _I64, _P, _SZ, _I, _P]),
     "dgf_profile_begin": (_I, [ctypes.POINTER(_P), _I]),
     "dgf_profile_end": (_I, []),
     "dgf_profile_name": (ctypes.c_char_p, [_I]),
@@ -342,6 +357,225 @@ def act_bwd(da, g, u, stream=None):
     else:
         _check(L.dgf_act_bwd_typed(*ptrs, dt, _stream(stream)), "dgf_act_bwd_typed")
     return dg, du, a
+
+
+# ------------------------------------------------- operators around the FFN
+def _vec(t, H: int, like: torch.Tensor, name: str):
+    """Pointer of a contiguous [H] vector of like's dtype (None: NULL)."""
+    if t is None:
+        return None
+    if t.dtype != like.dtype or t.device != like.device:
+        raise TypeError(f"{name}: expected {like.dtype} on {like.device}, got {t.dtype} on {t.device}")
+    if t.dim() != 1 or t.shape[0] != H or (H > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name}: expected a contiguous vector of {H} elements")
+    return t.data_ptr()
+
+
+def _rows(t, shape, like: torch.Tensor, name: str):
+    """(pointer, leading dimension) of a matrix of the given shape and like's dtype (None: NULL)."""
+    if t is None:
+        return None, 0
+    if t.dtype != like.dtype or t.device != like.device:
+        raise TypeError(f"{name}: expected {like.dtype} on {like.device}, got {t.dtype} on {t.device}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    return _mat(t, name)
+
+
+def _gate(gate, M: int, H: int, like: torch.Tensor):
+    """(pointer, leading dimension): 0 for one value a channel ([H])."""
+    if gate is not None and gate.dim() == 1:
+        return _vec(gate, H, like, "gate"), 0
+    return _rows(gate, (M, H), like, "gate")
+
+
+def norm_fwd(res, y=None, w_post=None, gate=None, alpha: float = 1.0, w_next=None, eps: float = 1e-6,
+             training: bool = False, out=None, stream=None):
+    """The norms after a block (of its output y, with gate and the residual res)
+    and before the next one, dgf_norm_fwd:
+
+        t = y r_y w_post;  z = alpha res + gate t;  h = z r_z w_next
+
+    res, y [M, H]; w_post, w_next [H]; gate [H] or [M, H]; w_post None: t = y;
+    gate None: 1; w_next None: no h; y None: h from res alone (z is res).
+    Returns a dict with z, h (w_next given) and rstd [M, 2] FP32 (training).
+    out: where z goes (may be res itself)."""
+    L = load()
+    dt = _stored(res)
+    M, H = res.shape
+    rp, ldr = _mat(res, "res")
+    yp, ldy = _rows(y, (M, H), res, "y")
+    gp, ldg = _gate(gate, M, H, res)
+    wp, wn = _vec(w_post, H, res, "w_post"), _vec(w_next, H, res, "w_next")
+    with _on(stream):
+        z = res if y is None else _empty(M, H, res) if out is None else out
+        h = _empty(M, H, res) if w_next is not None else None
+        rstd = torch.empty((M, 2), dtype=torch.float32, device=res.device) if training else None
+    zp, ldz = _rows(z, (M, H), res, "out")
+    hp, ldh = (h.data_ptr(), h.stride(0)) if h is not None else (None, 0)
+    _check(L.dgf_norm_fwd(rp, ldr, yp, ldy, wp, gp, ldg, alpha, wn, eps, zp, ldz, hp, ldh,
+                          rstd.data_ptr() if training else None, M, H, dt, _stream(stream)), "dgf_norm_fwd")
+    r = {"z": z}
+    if h is not None:
+        r["h"] = h
+    if training:
+        r["rstd"] = rstd
+    return r
+
+
+def norm_bwd(dz, dh, z, y=None, w_post=None, gate=None, alpha: float = 1.0, w_next=None, rstd=None, stream=None):
+    """Backward of norm_fwd (dgf_norm_bwd) from dz and dh (either may be None),
+    the forward's z and rstd and its inputs.  Returns a dict: dres, and dy,
+    dw_post, dgate, dw_next for the inputs that were given."""
+    L = load()
+    like = dz if dz is not None else dh
+    if like is None or rstd is None:
+        raise ValueError("norm_bwd needs dz or dh, and the forward's rstd")
+    dt = _stored(like)
+    M, H = like.shape
+    dzp, lddz = _rows(dz, (M, H), like, "dz")
+    dhp, lddh = _rows(dh, (M, H), like, "dh")
+    zp, ldz = _rows(z, (M, H), like, "z")
+    yp, ldy = _rows(y, (M, H), like, "y")
+    gp, ldg = _gate(gate, M, H, like)
+    wp, wn = _vec(w_post, H, like, "w_post"), _vec(w_next, H, like, "w_next")
+    if rstd.dtype != torch.float32 or tuple(rstd.shape) != (M, 2) or not rstd.is_contiguous() or rstd.device != like.device:
+        raise ValueError(f"rstd: expected the forward's contiguous float32 [{M}, 2]")
+    r = {}
+    with _on(stream):
+        r["dres"] = _empty(M, H, like)
+        if y is not None:
+            r["dy"] = _empty(M, H, like)
+        if w_post is not None:
+            r["dw_post"] = torch.empty(H, dtype=like.dtype, device=like.device)
+        if gate is not None:
+            r["dgate"] = torch.empty(H, dtype=like.dtype, device=like.device) if ldg == 0 else _empty(M, H, like)
+        if w_next is not None:
+            r["dw_next"] = torch.empty(H, dtype=like.dtype, device=like.device)
+        ws = _workspace(L.dgf_norm_bwd_workspace(M, H), like)
+    ptr = {k: t.data_ptr() for k, t in r.items()}
+    _check(L.dgf_norm_bwd(dzp, lddz, dhp, lddh, zp, ldz, yp, ldy, wp, gp, ldg, alpha, wn, rstd.data_ptr(),
+                          ptr["dres"], r["dres"].stride(0), ptr.get("dy"), r["dy"].stride(0) if y is not None else 0,
+                          ptr.get("dw_post"), ptr.get("dgate"), r["dgate"].stride(0) if ldg else 0,
+                          ptr.get("dw_next"), M, H, ws.data_ptr(), ws.numel(), dt, _stream(stream)), "dgf_norm_bwd")
+    return r
+
+
+BLOCK8 = 64  # columns that share a scale of an 8-bit checkpoint
+
+
+class Packed8(NamedTuple):
+    """A matrix [M, N] saved in 8 bits: codes (int8 [M, N], row-major), scales
+    (FP32 [M, ceil(N/64)]) and the type it reads back as."""
+
+    codes: torch.Tensor
+    scales: torch.Tensor
+    dtype: torch.dtype
+
+
+def _packed(M: int, N: int, like: torch.Tensor) -> Packed8:
+    ld = (N + 15) // 16 * 16
+    codes = torch.empty((M, ld), dtype=torch.int8, device=like.device)[:, :N]
+    return Packed8(codes, torch.empty((M, -(-N // BLOCK8)), dtype=torch.float32, device=like.device), like.dtype)
+
+
+def _q8(p: Packed8, shape, dtype, device, name: str):
+    """(codes, their leading dimension, scales, theirs) of a checkpoint of the given shape and type."""
+    q, s = p.codes, p.scales
+    M, N = shape
+    if p.dtype != dtype or q.dtype != torch.int8 or s.dtype != torch.float32 or q.device != device or s.device != device:
+        raise TypeError(f"{name}: expected an 8-bit checkpoint of {dtype} on {device} (int8 codes, float32 scales)")
+    if tuple(q.shape) != (M, N) or tuple(s.shape) != (M, -(-N // BLOCK8)):
+        raise ValueError(f"{name}: codes {tuple(q.shape)} and scales {tuple(s.shape)} are not those of a {M} x {N} matrix")
+    if (N > 1 and q.stride(1) != 1) or (s.shape[1] > 1 and s.stride(1) != 1):
+        raise ValueError(f"{name}: expected row-major codes and scales")
+    return q.data_ptr(), q.stride(0), s.data_ptr(), s.stride(0)
+
+
+def pack8(t, stream=None) -> Packed8:
+    """Saves a BF16 or FP16 matrix in 8 bits, blocks of 64 columns with an FP32 scale each (dgf_pack8)."""
+    L = load()
+    dt = _stored(t)
+    tp, ldt = _mat(t, "t")
+    M, N = t.shape
+    with _on(stream):
+        p = _packed(M, N, t)
+    _check(L.dgf_pack8(tp, ldt, p.codes.data_ptr(), p.codes.stride(0), p.scales.data_ptr(), p.scales.stride(0), M, N,
+                       dt, _stream(stream)), "dgf_pack8")
+    return p
+
+
+def unpack8(p: Packed8, stream=None) -> torch.Tensor:
+    """Reads an 8-bit checkpoint back in its stored type, each value rounded once (dgf_unpack8)."""
+    L = load()
+    if p.dtype not in _STORED:
+        raise TypeError(f"expected a checkpoint of bfloat16 or float16, got {p.dtype}")
+    M, N = p.codes.shape
+    qp, ldq, sp, lds = _q8(p, (M, N), p.dtype, p.codes.device, "p")
+    with _on(stream):
+        t = torch.empty((M, (N + 7) // 8 * 8), dtype=p.dtype, device=p.codes.device)[:, :N]
+    _check(L.dgf_unpack8(qp, ldq, sp, lds, t.data_ptr(), t.stride(0), M, N, _STORED[p.dtype], _stream(stream)),
+           "dgf_unpack8")
+    return t
+
+
+def act_bwd_q8(da, g: Packed8, u: Packed8, stream=None):
+    """act_bwd over a matrix [M, N] from g and u saved in 8 bits: dG, dU and the recomputed a."""
+    L = load()
+    dt = _stored(da)
+    M, N = da.shape
+    dap, ldda = _mat(da, "da")
+    gq, ldq, gs, lds = _q8(g, (M, N), da.dtype, da.device, "g")
+    uq, ldq2, us, lds2 = _q8(u, (M, N), da.dtype, da.device, "u")
+    if (ldq, lds) != (ldq2, lds2):
+        raise ValueError("g and u must share their leading dimensions")
+    with _on(stream):
+        dg, du, a = _empty(M, N, da), _empty(M, N, da), _empty(M, N, da)
+    _check(L.dgf_act_bwd_q8(dap, ldda, gq, gs, uq, us, ldq, lds, dg.data_ptr(), du.data_ptr(), a.data_ptr(),
+                            dg.stride(0), M, N, dt, _stream(stream)), "dgf_act_bwd_q8")
+    return dg, du, a
+
+
+def ffn_fwd_q8(x, w_gate, w_up, w_down, stream=None):
+    """The training forward with g and u saved in 8 bits (dgf_ffn_fwd_q8): y (the
+    bits of ffn_fwd) and the two checkpoints."""
+    L = load()
+    dt = _stored(x, w_gate, w_up, w_down)
+    M, H = x.shape
+    I = w_gate.shape[0]
+    xp, ldx = _mat(x, "x"); wg, ldwg = _rows(w_gate, (I, H), x, "w_gate"); wu, ldwu = _rows(w_up, (I, H), x, "w_up")
+    wd, ldwd = _rows(w_down, (H, I), x, "w_down")
+    with _on(stream):
+        y, g, u = _empty(M, H, x), _packed(M, I, x), _packed(M, I, x)
+        ws = _workspace(L.dgf_ffn_fwd_q8_workspace(M, H, I), x)
+    _check(L.dgf_ffn_fwd_q8(xp, ldx, wg, ldwg, wu, ldwu, wd, ldwd, y.data_ptr(), y.stride(0),
+                            g.codes.data_ptr(), g.scales.data_ptr(), u.codes.data_ptr(), u.scales.data_ptr(),
+                            g.codes.stride(0), g.scales.stride(0), M, H, I, ws.data_ptr(), ws.numel(), dt,
+                            _stream(stream)), "dgf_ffn_fwd_q8")
+    return y, g, u
+
+
+def ffn_bwd_q8(dy, x, g: Packed8, u: Packed8, w_gate, w_up, w_down, stream=None):
+    """ffn_bwd from the checkpoints of ffn_fwd_q8 (dgf_ffn_bwd_q8): dict dX, dW_gate, dW_up, dW_down."""
+    L = load()
+    dt = _stored(dy, x, w_gate, w_up, w_down)
+    M, H = x.shape
+    I = w_gate.shape[0]
+    dyp, lddy = _rows(dy, (M, H), x, "dy"); xp, ldx = _mat(x, "x")
+    wg, ldwg = _rows(w_gate, (I, H), x, "w_gate"); wu, ldwu = _rows(w_up, (I, H), x, "w_up")
+    wd, ldwd = _rows(w_down, (H, I), x, "w_down")
+    gq, ldq, gs, lds = _q8(g, (M, I), x.dtype, x.device, "g")
+    uq, ldq2, us, lds2 = _q8(u, (M, I), x.dtype, x.device, "u")
+    if (ldq, lds) != (ldq2, lds2):
+        raise ValueError("g and u must share their leading dimensions")
+    with _on(stream):
+        dx, dwg, dwu, dwd = _empty(M, H, x), _empty(I, H, x), _empty(I, H, x), _empty(H, I, x)
+        ws = _workspace(L.dgf_ffn_bwd_workspace(M, H, I), x)
+    _check(L.dgf_ffn_bwd_q8(dyp, lddy, xp, ldx, gq, gs, uq, us, ldq, lds, wg, ldwg, wu, ldwu, wd, ldwd,
+                            dx.data_ptr(), None, None, dx.stride(0), dwg.data_ptr(), dwg.stride(0),
+                            dwu.data_ptr(), dwu.stride(0), dwd.data_ptr(), dwd.stride(0), M, H, I,
+                            ws.data_ptr(), ws.numel(), dt, _stream(stream)), "dgf_ffn_bwd_q8")
+    return {"dX": dx, "dW_gate": dwg, "dW_up": dwu, "dW_down": dwd}
 
 
 class KernelTimer:

@@ -1,111 +1,19 @@
 // C ABI of libdgf: argument validation, workspace layout and the launch
 // sequence of the forward and backward passes (declarations in include/dgf.h).
-#include <stdarg.h>
-#include <stdio.h>
 #include <string.h>
 
 #include <mutex>
-#include <string>
 
-#include "dgf.h"
-#include "dgf_kernels.hpp"
+#include "dgf_host.hpp"
+#include "dgf_q8.hpp"
 
 using namespace dgf;
 
-namespace {
-
-thread_local std::string g_err;
-
-dgf_status fail(dgf_status st, const char *fmt, ...) {
-  char buf[512];
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(buf, sizeof buf, fmt, ap);
-  va_end(ap);
-  g_err = buf;
-  return st;
-}
-
-dgf_status ok() {
-  g_err.clear();
-  return DGF_OK;
-}
-
-dgf_status hip_check(hipError_t e, const char *what) {
-  if (e != hipSuccess) return fail(DGF_EHIP, "%s: %s", what, hipGetErrorString(e));
-  return DGF_OK;
-}
-
-}  // namespace
-
+thread_local std::string dgf::g_err;
+thread_local Prof dgf::g_prof;
 thread_local hipEvent_t dgf::g_launch_events[2] = {nullptr, nullptr};
 
 namespace {
-
-// Kernel timing hook: caller-created events, one pair per launch step (one
-// kernel, or a vector body and its scalar tail), recorded as the kernels' own
-// start and end timestamps.
-struct Prof {
-  hipEvent_t *ev = nullptr;
-  int pairs = 0;
-  int used = 0;
-  const char *names[4096] = {};
-};
-thread_local Prof g_prof;
-
-template <class F>
-hipError_t timed(hipStream_t s, const char *name, F &&launch) {
-  const int k = g_prof.used;
-  const bool rec = g_prof.ev && k < g_prof.pairs;
-  if (rec) {  // the launches record them as their kernels' start and end
-    g_launch_events[0] = g_prof.ev[2 * k];
-    g_launch_events[1] = g_prof.ev[2 * k + 1];
-  }
-  hipError_t e = launch();
-  if (rec) {
-    const bool none = g_launch_events[0] != nullptr;  // no kernel took them: an empty interval
-    g_launch_events[0] = g_launch_events[1] = nullptr;
-    if (none && e == hipSuccess) e = hipEventRecord(g_prof.ev[2 * k], s);
-    if (none && e == hipSuccess) e = hipEventRecord(g_prof.ev[2 * k + 1], s);
-  }
-  if (g_prof.ev) {
-    if (k < 4096) g_prof.names[k] = name;
-    g_prof.used = k + 1;
-  }
-  return e;
-}
-
-#define DGF_TRY(expr)                  \
-  do {                                 \
-    dgf_status st_ = (expr);           \
-    if (st_ != DGF_OK) return st_;     \
-  } while (0)
-
-bool aligned16(const void *p) { return ((uintptr_t)p & 15) == 0; }
-
-// A row-major BF16 matrix operand: non-null, 16-byte aligned, ld >= cols, ld % 8 == 0.
-constexpr int64_t kMaxLd = (int64_t)1 << 23;
-
-dgf_status check_mat(const char *name, const void *p, int64_t ld, int64_t rows, int64_t cols) {
-  if (rows == 0 || cols == 0) return DGF_OK;
-  if (!p) return fail(DGF_EINVAL, "%s is NULL", name);
-  if (!aligned16(p)) return fail(DGF_EINVAL, "%s is not 16-byte aligned", name);
-  if (ld < cols) return fail(DGF_EINVAL, "%s: leading dimension %lld < row width %lld", name, (long long)ld, (long long)cols);
-  if (ld % 8 != 0) return fail(DGF_EINVAL, "%s: leading dimension %lld is not a multiple of 8", name, (long long)ld);
-  // a 128-row tile's byte offsets from its first row stay below 2^31
-  if (ld >= kMaxLd) return fail(DGF_EUNSUPPORTED, "%s: leading dimension %lld beyond the library's limit (< 2^23)", name, (long long)ld);
-  return DGF_OK;
-}
-
-dgf_status check_dims(int64_t M, int64_t N, int64_t K) {
-  if (M < 0 || N < 0 || K < 0) return fail(DGF_EINVAL, "negative dimension (M=%lld N=%lld K=%lld)", (long long)M, (long long)N, (long long)K);
-  if (M > ((int64_t)1 << 21) || N > ((int64_t)1 << 30) || K > ((int64_t)1 << 23))
-    return fail(DGF_EUNSUPPORTED, "dimensions beyond the library's limits (M<=2^21, N<=2^30, K<=2^23)");
-  return DGF_OK;
-}
-
-int64_t round8(int64_t v) { return (v + 7) & ~(int64_t)7; }
-size_t round256(size_t v) { return (v + 255) & ~(size_t)255; }
 
 int leaves(int64_t K) { return (int)((K + 63) / 64); }
 
@@ -121,16 +29,6 @@ GemmParams blank(int fmt) {
   memset(&p, 0, sizeof p);
   p.fmt = fmt;
   return p;
-}
-
-// Public dtype code -> stored type of the kernels: BF16 and FP16 share the
-// tree; an FP32 FFN has no declared leaf rule (its MFMA differs), so it is
-// rejected as unsupported.
-dgf_status stored_type(int dtype, int *fmt) {
-  if (dtype == DGF_BF16) { *fmt = FMT_BF16; return DGF_OK; }
-  if (dtype == DGF_FP16) { *fmt = FMT_F16; return DGF_OK; }
-  if (dtype == DGF_FP32) return fail(DGF_EUNSUPPORTED, "dtype FP32: only BF16 and FP16 storage is implemented here");
-  return fail(DGF_EINVAL, "unknown dtype %d", dtype);
 }
 
 // Launch shape of one tree GEMM.  A wave owns 16 RT output columns (RT from
@@ -265,6 +163,12 @@ MmPlan plan_mm(int layout, int64_t M, int64_t K) {
   return pl;
 }
 
+// Whether a GEMM with an epilogue runs on the tiled or the streaming kernel,
+// whose roots go through a join (the generic kernels have their own epilogues).
+bool has_join(int layout, int nb, int64_t M, int64_t N, int64_t K) {
+  return plan_mm(layout, M, K).kd >= 0 || plan_xs(layout, nb, M, N, K).waves > 0;
+}
+
 // Workspace bytes for the partial roots of one GEMM (0 when it needs none).
 size_t partial_bytes(int layout, int nb, int epi, int64_t M, int64_t N, int64_t K) {
   if (M == 0 || N == 0) return 0;
@@ -284,14 +188,25 @@ size_t partial_bytes(int layout, int nb, int epi, int64_t M, int64_t N, int64_t 
   return round256((size_t)nb * ((size_t)1 << pl.kdepth) * M * round8(N) * 2);
 }
 
+// g and u of the FFN saved in 8 bits.
+struct Q8Saved {
+  Q8Mat g, u;
+};
+
 // One tree GEMM: the MFMA kernel, then (K split) the combine of the partials.
 // `partials` must hold partial_bytes() of workspace.
 // defer_join (EPI_DX on the streaming kernel, at most 8 K pieces): the join
 // is not launched; its arguments go to *defer_join and deferred is set, for
 // the weight-gradient launch to run.  dx_join (TN): that deferred join.
+// q8 (EPI_ACT, EPI_DSILU): g and u go to, or come from, 8-bit checkpoints.
 dgf_status run_gemm(int layout, int nb, int epi, GemmParams p, hipStream_t s, const char *what,
                     uint16_t *partials = nullptr, const char *join_what = "K-piece join",
-                    GemmParams *defer_join = nullptr, bool *deferred = nullptr, const GemmParams *dx_join = nullptr) {
+                    GemmParams *defer_join = nullptr, bool *deferred = nullptr, const GemmParams *dx_join = nullptr,
+                    const Q8Saved *q8 = nullptr) {
+  auto join = [&](const GemmParams &j) {
+    if (q8) return epi == EPI_ACT ? launch_join_act_q8(j, q8->g, q8->u, s) : launch_join_dsilu_q8(j, q8->g, q8->u, s);
+    return launch_combine_epi(epi, nb, j, s);
+  };
   if (p.M == 0 || p.N == 0) return DGF_OK;
   if ((p.M + 31) / 32 > 65535 || (p.N + 15) / 16 > 0x7fffffff)
     return fail(DGF_EUNSUPPORTED, "%s: %lld x %lld output exceeds the launch grid", what, (long long)p.M, (long long)p.N);
@@ -321,7 +236,7 @@ dgf_status run_gemm(int layout, int nb, int epi, GemmParams p, hipStream_t s, co
     }
     DGF_TRY(hip_check(timed(s, what, [&] { return launch_mm(p, nb, mp.nlh, s); }), what));
     if (joined)
-      DGF_TRY(hip_check(timed(s, join_what, [&] { return launch_combine_epi(epi, nb, p, s); }), join_what));
+      DGF_TRY(hip_check(timed(s, join_what, [&] { return join(p); }), join_what));
     return DGF_OK;
   }
   const XsPlan xp = plan_xs(layout, nb, p.M, p.N, p.K);
@@ -345,10 +260,11 @@ dgf_status run_gemm(int layout, int nb, int epi, GemmParams p, hipStream_t s, co
       return DGF_OK;
     }
     if (joined)
-      DGF_TRY(hip_check(timed(s, join_what, [&] { return launch_combine_epi(epi, nb, p, s); }), join_what));
+      DGF_TRY(hip_check(timed(s, join_what, [&] { return join(p); }), join_what));
     return DGF_OK;
   }
   if (epi == EPI_DX) return fail(DGF_EUNSUPPORTED, "%s: K=%lld is too deep for the lane kernel", what, (long long)p.K);
+  if (q8) return fail(DGF_EUNSUPPORTED, "%s: K=%lld is too deep for 8-bit checkpoints", what, (long long)p.K);
   const Plan pl = plan_gemm(layout, nb, epi, p.M, p.N, p.K);
   p.stack_slots = pl.slots;
   p.ksplit_depth = pl.kdepth;
@@ -389,16 +305,6 @@ dgf_status zero_mat(uint16_t *C, int64_t ldc, int64_t M, int64_t N, hipStream_t 
                    }),
                    "zero fill");
 }
-
-struct Carve {
-  char *base;
-  size_t used;
-  uint16_t *take(size_t elems) {
-    uint16_t *p = (uint16_t *)(base + used);
-    used += round256(elems * 2);
-    return p;
-  }
-};
 
 // The dX lanes run as one two-product kernel with the ordered add in its join
 // when the weight-streaming kernel applies, else as two GEMMs and an add.
@@ -446,6 +352,12 @@ size_t fwd_ws_bytes(int64_t M, int64_t H, int64_t I) {
   const size_t dn = allk_applies(M, H, I) ? 0 : partial_bytes(DGF_LAYOUT_NT, 1, EPI_STORE, M, H, I);  // down-projection partial roots
   return round256((size_t)M * round8(I) * 2)  // a [M, I]
          + (gu > dn ? gu : dn);               // the gate/up roots are joined before the down GEMM starts
+}
+
+// The forward with an 8-bit checkpoint keeps g and u in the workspace where
+// the gate/up kernel has no join to pack them in.
+size_t fwd_q8_ws_bytes(int64_t M, int64_t H, int64_t I) {
+  return fwd_ws_bytes(M, H, I) + (gu_act_applies(M, I, H) ? 2 * round256((size_t)M * round8(I) * 2) : 0);
 }
 
 size_t gemm_ws_bytes(int layout, int64_t M, int64_t N, int64_t K) {
@@ -529,7 +441,7 @@ namespace {
 dgf_status ffn_fwd_impl(int fmt, const void *x, int64_t ldx, const void *w_gate, int64_t ld_wg, const void *w_up,
                         int64_t ld_wu, const void *w_down, int64_t ld_wd, void *y, int64_t ldy, void *g_save,
                         void *u_save, int64_t ld_gu, int64_t M, int64_t H, int64_t I, void *ws, size_t ws_bytes,
-                        void *stream) {
+                        void *stream, const Q8Saved *q8 = nullptr) {
   DGF_TRY(check_dims(M, I, H));
   DGF_TRY(check_dims(M, H, I));
   if (H == 0 || I == 0) return fail(DGF_EINVAL, "H and I must be positive (H=%lld I=%lld)", (long long)H, (long long)I);
@@ -544,13 +456,24 @@ dgf_status ffn_fwd_impl(int fmt, const void *x, int64_t ldx, const void *w_gate,
     DGF_TRY(check_mat("g_save", g_save, ld_gu, M, I));
     DGF_TRY(check_mat("u_save", u_save, ld_gu, M, I));
   }
-  const size_t need = fwd_ws_bytes(M, H, I);
+  if (q8) {
+    DGF_TRY(check_q8("g", q8->g, M, I));
+    DGF_TRY(check_q8("u", q8->u, M, I));
+    if (!gu_act_applies(M, I, H) && !has_join(DGF_LAYOUT_NT, 2, M, I, H))
+      return fail(DGF_EUNSUPPORTED, "H=%lld is too deep for 8-bit checkpoints", (long long)H);
+  }
+  const size_t need = q8 ? fwd_q8_ws_bytes(M, H, I) : fwd_ws_bytes(M, H, I);
   if (!ws || ws_bytes < need || !aligned16(ws))
     return fail(DGF_EWORKSPACE, "forward workspace: need %zu bytes (16-byte aligned), got %zu", need, ws ? ws_bytes : 0);
   hipStream_t s = (hipStream_t)stream;
   Carve cv{(char *)ws, 0};
   uint16_t *a = cv.take((size_t)M * round8(I));
   const int64_t lda_ = round8(I);
+  if (q8 && gu_act_applies(M, I, H)) {
+    g_save = cv.take((size_t)M * lda_);
+    u_save = cv.take((size_t)M * lda_);
+    ld_gu = lda_;
+  }
   uint16_t *partials = (uint16_t *)((char *)ws + cv.used);
 
   if (gu_act_applies(M, I, H)) {
@@ -564,6 +487,10 @@ dgf_status ffn_fwd_impl(int fmt, const void *x, int64_t ldx, const void *w_gate,
     f.g = (uint16_t *)g_save; f.u = (uint16_t *)u_save; f.ldgu = ld_gu;
     f.M = M; f.N = I; f.K = H; f.L = leaves(H); f.fmt = fmt;
     DGF_TRY(hip_check(timed(s, "gate/up + act", [&] { return launch_gu_act(f, s); }), "gate/up + act"));
+    if (q8) {
+      DGF_TRY(hip_check(timed(s, "pack g", [&] { return launch_pack8(fmt, f.g, ld_gu, q8->g, M, I, s); }), "pack g"));
+      DGF_TRY(hip_check(timed(s, "pack u", [&] { return launch_pack8(fmt, f.u, ld_gu, q8->u, M, I, s); }), "pack u"));
+    }
   } else {
     GemmParams p = blank(fmt);
     p.A[0] = p.A[1] = (const uint16_t *)x;
@@ -579,7 +506,8 @@ dgf_status ffn_fwd_impl(int fmt, const void *x, int64_t ldx, const void *w_gate,
     p.act_out = a;
     p.ld_act = lda_;
     p.M = M; p.N = I; p.K = H;
-    DGF_TRY(run_gemm(DGF_LAYOUT_NT, 2, EPI_ACT, p, s, "gate/up tree GEMM", partials, "gate/up join + act"));
+    DGF_TRY(run_gemm(DGF_LAYOUT_NT, 2, EPI_ACT, p, s, "gate/up tree GEMM", partials, "gate/up join + act", nullptr, nullptr,
+                     nullptr, q8));
   }
 
   if (allk_applies(M, H, I)) {
@@ -658,7 +586,7 @@ dgf_status ffn_bwd_impl(int fmt, const void *dy, int64_t lddy, const void *x, in
                         int64_t ld_wu, const void *w_down, int64_t ld_wd, void *dx, void *dx_gate_lane,
                         void *dx_up_lane, int64_t lddx, void *dw_gate, int64_t ld_dwg, void *dw_up, int64_t ld_dwu,
                         void *dw_down, int64_t ld_dwd, int64_t M, int64_t H, int64_t I, void *ws, size_t ws_bytes,
-                        void *stream) {
+                        void *stream, const Q8Saved *q8 = nullptr) {
   DGF_TRY(check_dims(M, I, H));
   DGF_TRY(check_dims(M, H, I));
   if (H == 0 || I == 0) return fail(DGF_EINVAL, "H and I must be positive (H=%lld I=%lld)", (long long)H, (long long)I);
@@ -676,8 +604,15 @@ dgf_status ffn_bwd_impl(int fmt, const void *dy, int64_t lddy, const void *x, in
   }
   DGF_TRY(check_mat("dy", dy, lddy, M, H));
   DGF_TRY(check_mat("x", x, ldx, M, H));
-  DGF_TRY(check_mat("g", g, ld_gu, M, I));
-  DGF_TRY(check_mat("u", u, ld_gu, M, I));
+  if (q8) {
+    DGF_TRY(check_q8("g", q8->g, M, I));
+    DGF_TRY(check_q8("u", q8->u, M, I));
+    if (!has_join(nn_tiled(M) ? DGF_LAYOUT_NT : DGF_LAYOUT_NN, 1, M, I, H))
+      return fail(DGF_EUNSUPPORTED, "H=%lld is too deep for 8-bit checkpoints", (long long)H);
+  } else {
+    DGF_TRY(check_mat("g", g, ld_gu, M, I));
+    DGF_TRY(check_mat("u", u, ld_gu, M, I));
+  }
   DGF_TRY(check_mat("w_gate", w_gate, ld_wg, I, H));
   DGF_TRY(check_mat("w_up", w_up, ld_wu, I, H));
   DGF_TRY(check_mat("w_down", w_down, ld_wd, H, I));
@@ -742,7 +677,8 @@ dgf_status ffn_bwd_impl(int fmt, const void *dy, int64_t lddy, const void *x, in
   p.su = (const uint16_t *)u;
   p.ld_gu = ld_gu;
   p.dG = dG; p.dU = dU; p.a_rm = a_rm; p.ld_d = ld_d;
-  DGF_TRY(run_gemm(tiled ? DGF_LAYOUT_NT : DGF_LAYOUT_NN, 1, EPI_DSILU, p, s, "dA tree GEMM", partials, "dA join + dsilu"));
+  DGF_TRY(run_gemm(tiled ? DGF_LAYOUT_NT : DGF_LAYOUT_NN, 1, EPI_DSILU, p, s, "dA tree GEMM", partials, "dA join + dsilu",
+                   nullptr, nullptr, nullptr, q8));
   if (!direct) {  // token-major copies for the weight-gradient GEMMs
     DGF_TRY(hip_check(timed(s, "transpose dG", [&] { return launch_transpose(dG, ld_d, M, I, dGT, Mp, s); }), "transpose dG"));
     DGF_TRY(hip_check(timed(s, "transpose dU", [&] { return launch_transpose(dU, ld_d, M, I, dUT, Mp, s); }), "transpose dU"));
@@ -863,6 +799,36 @@ dgf_status dgf_ffn_bwd_typed(const void *dy, int64_t lddy, const void *x, int64_
   DGF_TRY(stored_type(dtype, &fmt));
   return ffn_bwd_impl(fmt, dy, lddy, x, ldx, g, u, ld_gu, w_gate, ld_wg, w_up, ld_wu, w_down, ld_wd, dx, dx_gate_lane,
                       dx_up_lane, lddx, dw_gate, ld_dwg, dw_up, ld_dwu, dw_down, ld_dwd, M, H, I, ws, ws_bytes, stream);
+}
+
+size_t dgf_ffn_fwd_q8_workspace(int64_t M, int64_t H, int64_t I) {
+  if (M <= 0 || H <= 0 || I <= 0) return 0;
+  return fwd_q8_ws_bytes(M, H, I);
+}
+
+dgf_status dgf_ffn_fwd_q8(const void *x, int64_t ldx, const void *w_gate, int64_t ld_wg, const void *w_up,
+                          int64_t ld_wu, const void *w_down, int64_t ld_wd, void *y, int64_t ldy, void *g_q, void *g_s,
+                          void *u_q, void *u_s, int64_t ld_q, int64_t ld_s, int64_t M, int64_t H, int64_t I, void *ws,
+                          size_t ws_bytes, int dtype, void *stream) {
+  int fmt = 0;
+  DGF_TRY(stored_type(dtype, &fmt));
+  const Q8Saved q8{{(uint8_t *)g_q, (float *)g_s, ld_q, ld_s}, {(uint8_t *)u_q, (float *)u_s, ld_q, ld_s}};
+  return ffn_fwd_impl(fmt, x, ldx, w_gate, ld_wg, w_up, ld_wu, w_down, ld_wd, y, ldy, nullptr, nullptr, 0, M, H, I, ws,
+                      ws_bytes, stream, &q8);
+}
+
+dgf_status dgf_ffn_bwd_q8(const void *dy, int64_t lddy, const void *x, int64_t ldx, const void *g_q, const void *g_s,
+                          const void *u_q, const void *u_s, int64_t ld_q, int64_t ld_s, const void *w_gate,
+                          int64_t ld_wg, const void *w_up, int64_t ld_wu, const void *w_down, int64_t ld_wd, void *dx,
+                          void *dx_gate_lane, void *dx_up_lane, int64_t lddx, void *dw_gate, int64_t ld_dwg,
+                          void *dw_up, int64_t ld_dwu, void *dw_down, int64_t ld_dwd, int64_t M, int64_t H, int64_t I,
+                          void *ws, size_t ws_bytes, int dtype, void *stream) {
+  int fmt = 0;
+  DGF_TRY(stored_type(dtype, &fmt));
+  const Q8Saved q8{{(uint8_t *)g_q, (float *)g_s, ld_q, ld_s}, {(uint8_t *)u_q, (float *)u_s, ld_q, ld_s}};
+  return ffn_bwd_impl(fmt, dy, lddy, x, ldx, nullptr, nullptr, 0, w_gate, ld_wg, w_up, ld_wu, w_down, ld_wd, dx,
+                      dx_gate_lane, dx_up_lane, lddx, dw_gate, ld_dwg, dw_up, ld_dwu, dw_down, ld_dwd, M, H, I, ws,
+                      ws_bytes, stream, &q8);
 }
 
 dgf_status dgf_tree_combine(const void *const *parts, int S, void *out, int64_t n, void *stream) {

@@ -1,0 +1,47 @@
+// Kernel interfaces of the operators around the FFN (internal; the public ABI
+// is include/dgf.h): the norms before and after a block.
+#pragma once
+
+#include "dgf_kernels.hpp"
+
+namespace dgf {
+
+// Widest row of the norm kernels: a row lives in the registers of one
+// workgroup, 16 elements a thread of 1024.
+constexpr int64_t kNormMaxH = 16384;
+
+struct NormFwdParams {
+  const uint16_t *res, *y;              // [M, H]; y null: z = res, only h is written
+  const uint16_t *w_post, *gate, *w_next;  // [H]; gate [M, H] with ld_gate > 0; any may be null
+  int64_t ld_res, ld_y, ld_gate;
+  uint16_t *z, *h;                      // [M, H]
+  int64_t ld_z, ld_h;
+  float *rstd;                          // [M, 2]: post, next; or null
+  float alpha, eps;
+  int64_t M, H;
+  int fmt;
+};
+hipError_t launch_norm_fwd(const NormFwdParams &p, hipStream_t s);
+
+struct NormBwdParams {
+  const uint16_t *dz, *dh, *z, *y;      // [M, H]; dz or dh may be null, y null as in the forward
+  const uint16_t *w_post, *gate, *w_next;
+  int64_t ld_dz, ld_dh, ld_z, ld_y, ld_gate;
+  const float *rstd;                    // [M, 2]
+  uint16_t *dres, *dy;                  // [M, H]
+  int64_t ld_dres, ld_dy;
+  uint16_t *dgate;                      // [M, H] when ld_gate > 0 (ld_dgate), else [H]; or null
+  int64_t ld_dgate;
+  uint16_t *dw_post, *dw_next;          // [H] or null
+  float *part;                          // [3][groups][round8(H)]: dw_post, dw_next, dgate
+  int groups;
+  float alpha;
+  int64_t M, H;
+  int fmt;
+};
+// Workgroups of the backward, each adding up its own rows' part of the column sums.
+int norm_bwd_groups(int64_t M, int64_t H);
+hipError_t launch_norm_bwd(const NormBwdParams &p, hipStream_t s);
+hipError_t launch_norm_wgrad(const NormBwdParams &p, hipStream_t s);
+
+}  // namespace dgf

@@ -223,6 +223,95 @@ dgf_status dgf_act_bwd_typed(const void *da, const void *g, const void *u, void 
                              int dtype, void *stream);
 
 /*
+ * Operators around the FFN.  Conventions as above: row-major stored-type
+ * matrices (dtype DGF_BF16 or DGF_FP16) with a leading dimension that is a
+ * multiple of 8 on a 16-byte aligned base, caller-owned buffers, status codes,
+ * calls that only enqueue work.  Every sum, scale and statistic is FP32; each
+ * output is rounded once; there are no atomics, so results are bitwise
+ * reproducible.  Their sums are plain FP32 sums in a fixed order, not the
+ * canonical tree of the FFN.
+ */
+
+/*
+ * The norms before and after a block, with its gate and residual.  res [M,H]
+ * is the residual stream, y [M,H] the block's output, w_post and w_next [H]:
+ *   t = y r_y w_post,  r_y = 1/sqrt(mean(y^2) + eps)   (w_post NULL: t = y, r_y = 1)
+ *   z = alpha res + gate t                             (gate NULL: gate = 1)
+ *   h = z r_z w_next,  r_z = 1/sqrt(mean(z^2) + eps)   (w_next, h NULL: no h)
+ * gate is one value a channel ([H], ld_gate = 0) or one an element ([M,H],
+ * ld_gate >= H).  y NULL: the norm before a block alone, h from z = res (no z
+ * is written; w_post and gate NULL, alpha 1).  h is taken from z before z is
+ * rounded.  rstd [M,2] (r_y, r_z; r = 1 where there is no norm) is optional
+ * and is what the backward needs.  z may be res itself (in place).  H is at
+ * most 16384 (else DGF_EUNSUPPORTED); eps is positive.  M = 0: DGF_OK, no launch.
+ */
+dgf_status dgf_norm_fwd(const void *res, int64_t ld_res, const void *y, int64_t ld_y, const void *w_post,
+                        const void *gate, int64_t ld_gate, float alpha, const void *w_next, float eps, void *z,
+                        int64_t ld_z, void *h, int64_t ld_h, float *rstd, int64_t M, int64_t H, int dtype,
+                        void *stream);
+
+/*
+ * Its backward from dz and dh (either may be NULL, not both; dh with w_next),
+ * the forward's z (res when y was NULL; not read when dh is NULL), y, weights,
+ * gate, alpha and rstd:
+ *   G = dz + r_z (dn - z r_z^2 mean(dn z)),  dn = dh w_next
+ *   dres = alpha G,  dgate = G t,  dq = G gate w_post
+ *   dy = r_y (dq - y r_y^2 mean(dq y))                 (w_post NULL: dy = G gate)
+ *   dw_post = sum over rows of G gate y r_y,  dw_next = sum over rows of dh z r_z
+ * dgate is [H] (the sum over rows) for ld_gate = 0, else [M,H] (ld_dgate).
+ * dw_post, dgate and dw_next may each be NULL; dres is always written, dy when
+ * y is given.  dres may be dz itself.  Workspace: dgf_norm_bwd_workspace(M,H)
+ * bytes.  M = 0: the sums over rows are written as +0.
+ */
+size_t dgf_norm_bwd_workspace(int64_t M, int64_t H);
+dgf_status dgf_norm_bwd(const void *dz, int64_t ld_dz, const void *dh, int64_t ld_dh, const void *z, int64_t ld_z,
+                        const void *y, int64_t ld_y, const void *w_post, const void *gate, int64_t ld_gate,
+                        float alpha, const void *w_next, const float *rstd, void *dres, int64_t ld_dres, void *dy,
+                        int64_t ld_dy, void *dw_post, void *dgate, int64_t ld_dgate, void *dw_next, int64_t M,
+                        int64_t H, void *ws, size_t ws_bytes, int dtype, void *stream);
+
+/*
+ * Activation checkpoints in 8 bits.  A row of N columns is cut into blocks of
+ * 64 (the last may be short).  A block with largest magnitude A keeps the FP32
+ * scale s = A/127 and one signed byte a value, q = rint(x (127/A)); it reads
+ * back as q s, at most s/2 (up to FP32 rounding) from x.  A block with
+ * A < 2^-119 keeps s = 0 and reads back as +0; one that holds an infinity or a
+ * NaN keeps s = NaN and reads back as NaN throughout.
+ * codes: [M,N] bytes, leading dimension ld_q a multiple of 8, 16-byte aligned;
+ * scales: [M, ceil(N/64)] FP32 with leading dimension ld_s.
+ */
+dgf_status dgf_pack8(const void *x, int64_t ldx, void *q, int64_t ld_q, float *scales, int64_t ld_s, int64_t M,
+                     int64_t N, int dtype, void *stream);
+dgf_status dgf_unpack8(const void *q, int64_t ld_q, const float *scales, int64_t ld_s, void *x, int64_t ldx, int64_t M,
+                       int64_t N, int dtype, void *stream);
+
+/* dgf_act_bwd over [M,N] from g and u in 8 bits: they are read back in FP32
+ * and not rounded to the stored type.  a (NULL to skip), dg and du share ld_out. */
+dgf_status dgf_act_bwd_q8(const void *da, int64_t ldda, const void *g_q, const float *g_s, const void *u_q,
+                          const float *u_s, int64_t ld_q, int64_t ld_s, void *dg, void *du, void *a, int64_t ld_out,
+                          int64_t M, int64_t N, int dtype, void *stream);
+
+/*
+ * The FFN's training forward and backward with g and u saved in 8 bits (codes
+ * [M,I] with ld_q, scales with ld_s).  The forward's y has the bits of
+ * dgf_ffn_fwd, the checkpoint those of dgf_pack8 over the g and u it would
+ * have saved.  The backward is dgf_ffn_bwd with dG, dU and a as
+ * dgf_act_bwd_q8 gives them.  Arguments otherwise as for those calls
+ * (dgf_ffn_bwd_workspace serves the backward).  H up to 65536.
+ */
+size_t dgf_ffn_fwd_q8_workspace(int64_t M, int64_t H, int64_t I);
+dgf_status dgf_ffn_fwd_q8(const void *x, int64_t ldx, const void *w_gate, int64_t ld_wg, const void *w_up,
+                          int64_t ld_wu, const void *w_down, int64_t ld_wd, void *y, int64_t ldy, void *g_q, void *g_s,
+                          void *u_q, void *u_s, int64_t ld_q, int64_t ld_s, int64_t M, int64_t H, int64_t I, void *ws,
+                          size_t ws_bytes, int dtype, void *stream);
+dgf_status dgf_ffn_bwd_q8(const void *dy, int64_t lddy, const void *x, int64_t ldx, const void *g_q, const void *g_s,
+                          const void *u_q, const void *u_s, int64_t ld_q, int64_t ld_s, const void *w_gate,
+                          int64_t ld_wg, const void *w_up, int64_t ld_wu, const void *w_down, int64_t ld_wd, void *dx,
+                          void *dx_gate_lane, void *dx_up_lane, int64_t lddx, void *dw_gate, int64_t ld_dwg,
+                          void *dw_up, int64_t ld_dwu, void *dw_down, int64_t ld_dwd, int64_t M, int64_t H, int64_t I,
+                          void *ws, size_t ws_bytes, int dtype, void *stream);
+
+/*
  * Diagnostic entry points (stage isolation and shard emulation; the FFN
  * entry points above are composed of the same kernels).
  *
