@@ -66,6 +66,9 @@ SIGNATURES = {
     "dgf_ffn_bwd_q8": (_I, [_P, _I64, _P, _I64, _P, _P, _P, _P, _I64, _I64, _P, _I64, _P, _I64, _P, _I64,
                             _P, _P, _P, _I64, _P, _I64, _P, _I64, _P, _I64,
                             _I64, _I64, _I64, _P, _SZ, _I, _P]),
+    "dgf_moe_fwd_workspace": (_SZ, [_I64, _I64, _I64, _I64, _I64, _I64]),
+    "dgf_moe_fwd": (_I, [_P, _I64, _P, _I64, _P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _P, _I64, _P, _P,
+                         _I64, _I64, _I64, _I64, _I64, _I64, _I64, _I, _P, _SZ, _I, _P]),
     "dgf_profile_begin": (_I, [ctypes.POINTER(_P), _I]),
     "dgf_profile_end": (_I, []),
     "dgf_profile_name": (ctypes.c_char_p, [_I]),
@@ -576,6 +579,48 @@ def ffn_bwd_q8(dy, x, g: Packed8, u: Packed8, w_gate, w_up, w_down, stream=None)
                             dwu.data_ptr(), dwu.stride(0), dwd.data_ptr(), dwd.stride(0), M, H, I,
                             ws.data_ptr(), ws.numel(), dt, _stream(stream)), "dgf_ffn_bwd_q8")
     return {"dX": dx, "dW_gate": dwg, "dW_up": dwu, "dW_down": dwd}
+
+
+def _experts(t: torch.Tensor, shape, like: torch.Tensor, name: str):
+    """(pointer, leading dimension, expert stride) of the experts' matrices [El, rows, cols]."""
+    if t.dtype != like.dtype or t.device != like.device:
+        raise TypeError(f"{name}: expected {like.dtype} on {like.device}, got {t.dtype} on {t.device}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.stride(2) != 1:
+        raise ValueError(f"{name}: expected row-major matrices (stride(2) == 1)")
+    return t.data_ptr(), t.stride(1), t.stride(0)
+
+
+def moe_fwd(x, w_router, w_gate, w_up, w_down, top_k: int, renorm: bool = True, routing: bool = False,
+            expert_offset: int = 0, stream=None):
+    """A mixture-of-experts layer of gated FFNs for up to 128 tokens (dgf_moe_fwd).
+
+    x [M, H]; w_router [E, H]; w_gate, w_up [El, I, H] and w_down [El, H, I], the
+    experts [expert_offset, expert_offset + El) of the E (all of them by default).
+    renorm: routing weights over the top_k chosen instead of all E.
+    Returns y [M, H], or with routing (y, ids int32 [M, top_k], weights float32 [M, top_k])."""
+    L = load()
+    dt = _stored(x)
+    M, H = x.shape
+    E, (El, I) = w_router.shape[0], w_gate.shape[:2]
+    xp, ldx = _mat(x, "x")
+    wr, ldr = _rows(w_router, (E, H), x, "w_router")
+    wg, ldg, sg = _experts(w_gate, (El, I, H), x, "w_gate")
+    wu, ldu, su = _experts(w_up, (El, I, H), x, "w_up")
+    wd, ldd, sd = _experts(w_down, (El, H, I), x, "w_down")
+    ids = probs = None
+    with _on(stream):
+        y = _empty(M, H, x)
+        if routing:
+            ids = torch.empty((M, max(top_k, 0)), dtype=torch.int32, device=x.device)
+            probs = torch.empty((M, max(top_k, 0)), dtype=torch.float32, device=x.device)
+        ws = _workspace(L.dgf_moe_fwd_workspace(M, H, I, E, El, top_k), x)
+    _check(L.dgf_moe_fwd(xp, ldx, wr, ldr, wg, ldg, sg, wu, ldu, su, wd, ldd, sd, y.data_ptr(), y.stride(0),
+                         ids.data_ptr() if routing else None, probs.data_ptr() if routing else None,
+                         M, H, I, E, expert_offset, El, top_k, int(renorm), ws.data_ptr(), ws.numel(), dt,
+                         _stream(stream)), "dgf_moe_fwd")
+    return (y, ids, probs) if routing else y
 
 
 class KernelTimer:

@@ -17,7 +17,7 @@ LIB = os.path.join(PKG, "libdgf.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 
 SOURCES = ["dgf_gemm.hip", "dgf_xs.hip", "dgf_gu.hip", "dgf_mm.hip", "dgf_dn.hip", "dgf_elementwise.hip", "dgf_norm.hip",
-           "dgf_q8.hip", "dgf_api.hip", "dgf_block_api.hip"]
+           "dgf_q8.hip", "dgf_moe.hip", "dgf_api.hip", "dgf_block_api.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

@@ -1,5 +1,6 @@
 // Kernel interfaces of the operators around the FFN (internal; the public ABI
-// is include/dgf.h): the norms before and after a block.
+// is include/dgf.h): the norms before and after a block, and the
+// mixture-of-experts layer for a few tokens.
 #pragma once
 
 #include "dgf_kernels.hpp"
@@ -43,5 +44,33 @@ struct NormBwdParams {
 int norm_bwd_groups(int64_t M, int64_t H);
 hipError_t launch_norm_bwd(const NormBwdParams &p, hipStream_t s);
 hipError_t launch_norm_wgrad(const NormBwdParams &p, hipStream_t s);
+
+// Mixture of experts (dgf_moe.hip): E experts in all, of which this call holds
+// the weights of [e0, e0 + El).  Limits: M tokens, k experts a token, E.
+constexpr int kMoeMaxM = 128, kMoeMaxK = 16, kMoeMaxE = 1024;
+struct MoeParams {
+  const uint16_t *x, *w_router;              // [M, H], [E, H]
+  const uint16_t *w_gate, *w_up, *w_down;    // [El, I, H], [El, I, H], [El, H, I]
+  int64_t ldx, ld_wr, ld_wg, ld_wu, ld_wd;
+  int64_t st_wg, st_wu, st_wd;               // elements from one expert to the next
+  uint16_t *y;                               // [M, H]
+  int64_t ldy;
+  int *ids_out;                              // [M, k] or null
+  float *p_out;                              // [M, k] or null
+  int M, H, I, E, e0, El, k, renorm, fmt;
+  // workspace
+  float *logits;                             // [M, E]
+  float *p;                                  // [M k] routing weights
+  int *ids;                                  // [M k] chosen experts
+  int *active;                               // [1 + El]: how many local experts have tokens, then which
+  int *count;                                // [El] tokens of a local expert
+  int *pairs;                                // [El, M]: its (token, choice) pairs m k + j, ascending
+  uint16_t *a_hi, *a_lo;                     // [M k, lda] the experts' activations in two parts
+  int64_t lda;
+};
+hipError_t launch_moe_logits(const MoeParams &p, hipStream_t s);
+hipError_t launch_moe_route(const MoeParams &p, hipStream_t s);
+hipError_t launch_moe_gate_up(const MoeParams &p, hipStream_t s);
+hipError_t launch_moe_down(const MoeParams &p, hipStream_t s);
 
 }  // namespace dgf

@@ -1,5 +1,5 @@
-// C ABI of the operators around the FFN: the norms before and after a block
-// and the 8-bit activation checkpoints (declarations in include/dgf.h).
+// C ABI of the operators around the FFN: the norms before and after a block,
+// the 8-bit activation checkpoints and the mixture of experts (declarations in include/dgf.h).
 #include "dgf_block.hpp"
 #include "dgf_host.hpp"
 #include "dgf_q8.hpp"
@@ -25,6 +25,43 @@ dgf_status check_norm(const void *y, const void *w_post, const void *gate, int64
   DGF_TRY(check_vec("w_post", w_post, false));
   if (gate && ld_gate != 0 && M > 0) DGF_TRY(check_mat("gate", gate, ld_gate, M, H));
   return check_vec("gate", gate, false);
+}
+
+// Workspace of the mixture of experts, laid out from ws (null: size only).
+size_t carve_moe(MoeParams &p, void *ws) {
+  Carve cv{(char *)ws, 0};
+  const size_t pairs = (size_t)p.M * p.k;
+  p.lda = round8(p.I);
+  p.logits = (float *)cv.take((size_t)p.M * p.E * 2);
+  p.p = (float *)cv.take(pairs * 2);
+  p.ids = (int *)cv.take(pairs * 2);
+  p.active = (int *)cv.take((size_t)(p.El + 1) * 2);
+  p.count = (int *)cv.take((size_t)p.El * 2);
+  p.pairs = (int *)cv.take((size_t)p.El * p.M * 2);
+  p.a_hi = cv.take(pairs * p.lda);
+  p.a_lo = cv.take(pairs * p.lda);
+  return cv.used;
+}
+
+dgf_status check_moe(int64_t M, int64_t H, int64_t I, int64_t E, int64_t e0, int64_t El, int64_t k) {
+  DGF_TRY(check_dims(M, H, I));
+  if (H == 0 || I == 0 || E <= 0) return fail(DGF_EINVAL, "H, I and E must be positive (H=%lld I=%lld E=%lld)", (long long)H, (long long)I, (long long)E);
+  if (k < 1 || k > E) return fail(DGF_EINVAL, "k=%lld experts a token: need 1 to E=%lld", (long long)k, (long long)E);
+  if (e0 < 0 || El < 1 || El > E || e0 > E - El)
+    return fail(DGF_EINVAL, "experts [%lld, %lld + %lld) are not within the %lld of the router", (long long)e0, (long long)e0, (long long)El, (long long)E);
+  if (M > kMoeMaxM || k > kMoeMaxK || E > kMoeMaxE || H > kMaxLd || I > kMaxLd)
+    return fail(DGF_EUNSUPPORTED, "mixture of experts for a few tokens: M <= %d, k <= %d, E <= %d, H and I <= 2^23 (M=%lld k=%lld E=%lld)",
+                kMoeMaxM, kMoeMaxK, kMoeMaxE, (long long)M, (long long)k, (long long)E);
+  return DGF_OK;
+}
+
+// The experts' matrices, `stride` elements apart.
+dgf_status check_experts(const char *name, const void *w, int64_t ld, int64_t stride, int64_t El, int64_t rows,
+                         int64_t cols) {
+  DGF_TRY(check_mat(name, w, ld, rows, cols));
+  if (El > 1 && (stride < (rows - 1) * ld + cols || stride % 8 != 0))
+    return fail(DGF_EINVAL, "%s: expert stride %lld: need a multiple of 8 past the %lld rows", name, (long long)stride, (long long)rows);
+  return DGF_OK;
 }
 
 }  // namespace
@@ -179,6 +216,53 @@ dgf_status dgf_act_bwd_q8(const void *da, int64_t ldda, const void *g_q, const f
   p.ldo = ld_out; p.M = M; p.N = N;
   hipStream_t s = (hipStream_t)stream;
   DGF_TRY(hip_check(timed(s, "act_bwd_q8", [&] { return launch_act_bwd_q8(fmt, p, s); }), "act_bwd_q8"));
+  return ok();
+}
+
+size_t dgf_moe_fwd_workspace(int64_t M, int64_t H, int64_t I, int64_t E, int64_t El, int64_t k) {
+  if (M <= 0 || H <= 0 || I <= 0 || E <= 0 || El <= 0 || k <= 0 || M > kMoeMaxM || E > kMoeMaxE || k > kMoeMaxK ||
+      El > E || I > kMaxLd)
+    return 0;
+  MoeParams p{};
+  p.M = (int)M; p.I = (int)I; p.E = (int)E; p.El = (int)El; p.k = (int)k;
+  return carve_moe(p, nullptr);
+}
+
+dgf_status dgf_moe_fwd(const void *x, int64_t ldx, const void *w_router, int64_t ld_wr, const void *w_gate,
+                       int64_t ld_wg, int64_t stride_wg, const void *w_up, int64_t ld_wu, int64_t stride_wu,
+                       const void *w_down, int64_t ld_wd, int64_t stride_wd, void *y, int64_t ldy, int32_t *ids,
+                       float *probs, int64_t M, int64_t H, int64_t I, int64_t E, int64_t e0, int64_t El, int64_t k,
+                       int renorm, void *ws, size_t ws_bytes, int dtype, void *stream) {
+  int fmt = 0;
+  DGF_TRY(stored_type(dtype, &fmt));
+  DGF_TRY(check_moe(M, H, I, E, e0, El, k));
+  if (M == 0) return ok();
+  DGF_TRY(check_mat("x", x, ldx, M, H));
+  DGF_TRY(check_mat("w_router", w_router, ld_wr, E, H));
+  DGF_TRY(check_experts("w_gate", w_gate, ld_wg, stride_wg, El, I, H));
+  DGF_TRY(check_experts("w_up", w_up, ld_wu, stride_wu, El, I, H));
+  DGF_TRY(check_experts("w_down", w_down, ld_wd, stride_wd, El, H, I));
+  DGF_TRY(check_mat("y", y, ldy, M, H));
+  if (((uintptr_t)ids | (uintptr_t)probs) & 3) return fail(DGF_EINVAL, "ids and probs must be 4-byte aligned");
+  const size_t need = dgf_moe_fwd_workspace(M, H, I, E, El, k);
+  if (!ws || ws_bytes < need || !aligned16(ws))
+    return fail(DGF_EWORKSPACE, "mixture of experts workspace: need %zu bytes (16-byte aligned), got %zu", need, ws ? ws_bytes : 0);
+  MoeParams p{};
+  p.x = (const uint16_t *)x; p.ldx = ldx;
+  p.w_router = (const uint16_t *)w_router; p.ld_wr = ld_wr;
+  p.w_gate = (const uint16_t *)w_gate; p.ld_wg = ld_wg; p.st_wg = stride_wg;
+  p.w_up = (const uint16_t *)w_up; p.ld_wu = ld_wu; p.st_wu = stride_wu;
+  p.w_down = (const uint16_t *)w_down; p.ld_wd = ld_wd; p.st_wd = stride_wd;
+  p.y = (uint16_t *)y; p.ldy = ldy;
+  p.ids_out = ids; p.p_out = probs;
+  p.M = (int)M; p.H = (int)H; p.I = (int)I; p.E = (int)E; p.e0 = (int)e0; p.El = (int)El; p.k = (int)k;
+  p.renorm = renorm != 0; p.fmt = fmt;
+  carve_moe(p, ws);
+  hipStream_t s = (hipStream_t)stream;
+  DGF_TRY(hip_check(timed(s, "moe logits", [&] { return launch_moe_logits(p, s); }), "moe logits"));
+  DGF_TRY(hip_check(timed(s, "moe route", [&] { return launch_moe_route(p, s); }), "moe route"));
+  DGF_TRY(hip_check(timed(s, "moe gate/up", [&] { return launch_moe_gate_up(p, s); }), "moe gate/up"));
+  DGF_TRY(hip_check(timed(s, "moe down", [&] { return launch_moe_down(p, s); }), "moe down"));
   return ok();
 }
 

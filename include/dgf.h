@@ -312,6 +312,33 @@ dgf_status dgf_ffn_bwd_q8(const void *dy, int64_t lddy, const void *x, int64_t l
                           void *ws, size_t ws_bytes, int dtype, void *stream);
 
 /*
+ * A mixture-of-experts layer for a few tokens, every expert the gated FFN.
+ * x [M,H], w_router [E,H]; this call holds the experts [e0, e0 + El) (all of
+ * them: e0 = 0, El = E): w_gate, w_up [El,I,H] and w_down [El,H,I], each expert
+ * a matrix with a leading dimension, stride_* elements (a multiple of 8) from
+ * one to the next.
+ *   l = x w_router^T (FP32); a token's experts e_0..e_{k-1} have its k largest
+ *   logits, in descending order, ties to the lowest index (NaN last)
+ *   p_j = softmax(l) at e_j over all E experts, or over the k chosen (renorm != 0)
+ *   a_j = silu(w_gate[e_j] x) (w_up[e_j] x);  y = sum over j of p_j w_down[e_j] a_j
+ * The sum takes the experts this call holds; a token with none of them gets
+ * y = +0, and the calls over all shards of the experts add up to the layer.
+ * ids (int32) and probs (FP32), both [M,k] and optional, are the routing over
+ * all E.  The products' sums and a's are FP32 (a passes between kernels with
+ * twice the stored type's bits); y is rounded once.  Row m of every output
+ * depends on row m of x only, bit for bit, whatever M is, so more than 128
+ * tokens can be given in pieces.
+ * Limits: M <= 128, k <= 16, E <= 1024 (else DGF_EUNSUPPORTED).  Workspace:
+ * dgf_moe_fwd_workspace bytes.  M = 0: DGF_OK, no launch.
+ */
+size_t dgf_moe_fwd_workspace(int64_t M, int64_t H, int64_t I, int64_t E, int64_t El, int64_t k);
+dgf_status dgf_moe_fwd(const void *x, int64_t ldx, const void *w_router, int64_t ld_wr, const void *w_gate,
+                       int64_t ld_wg, int64_t stride_wg, const void *w_up, int64_t ld_wu, int64_t stride_wu,
+                       const void *w_down, int64_t ld_wd, int64_t stride_wd, void *y, int64_t ldy, int32_t *ids,
+                       float *probs, int64_t M, int64_t H, int64_t I, int64_t E, int64_t e0, int64_t El, int64_t k,
+                       int renorm, void *ws, size_t ws_bytes, int dtype, void *stream);
+
+/*
  * Diagnostic entry points (stage isolation and shard emulation; the FFN
  * entry points above are composed of the same kernels).
  *

@@ -1,0 +1,208 @@
+"""GPU: the mixture-of-experts layer for a few tokens (moe_fwd) against FP64.
+
+Tolerances, derived before any run.  A product over K runs on the matrix core in
+blocks of 8: a block cuts its products and its accumulator to a grid 2^-24 of
+its largest term and rounds once, at most 10 2^-24 (m + S) for products of
+magnitude sum S and largest m, so over K / 8 blocks shared by up to 8 waves at
+most 10 (K / 64 + 1) + 16 units of 2^-24 S.  A logit (FP32 multiply-adds, K / 64
+a lane and 6 across lanes) is off by at most (K / 64 + 14) 2^-24 S.  The
+activation has slope at most 1.1 in g, times u, and 1.1 |g| in u; what is passed
+between the kernels keeps a to 2^-16 (BF16) or 2^-22 (FP16) of it.  y is rounded
+once: u = 2^-8 (BF16), 2^-11 (FP16).  Over a whole output rounding errors are
+spread evenly, so their relative 2-norm is below u."""
+import pytest
+import torch
+
+from deterministic_gated_ffn_amd import binding as dgf
+
+pytestmark = pytest.mark.gpu
+
+BF, FH = torch.bfloat16, torch.float16
+U = {BF: 2.0 ** -8, FH: 2.0 ** -11}
+KEEP = {BF: 2.0 ** -16, FH: 2.0 ** -22}
+EPS = 2.0 ** -24
+
+
+@pytest.fixture(scope="module", autouse=True)
+def gpu():
+    if not torch.cuda.is_available():
+        pytest.fail("no GPU visible: the GPU tests need an MI355X")
+    dgf.load()
+
+
+def rows(gen, shape, dt, scale=1.0, pad=0):
+    """Row-major, leading dimension a multiple of 8, NaN in the padding."""
+    ld = -(-shape[-1] // 8) * 8 + pad
+    buf = torch.full((*shape[:-1], ld), float("nan"), dtype=dt)
+    buf[..., :shape[-1]] = (torch.randn(shape, generator=gen) * scale).to(dt)
+    return buf.cuda()[..., :shape[-1]]
+
+
+def make(M, H, I, E, dt, seed=0, pad=0):
+    gen = torch.Generator().manual_seed(seed)
+    return (rows(gen, (M, H), dt, pad=pad), rows(gen, (E, H), dt, H ** -0.5),
+            rows(gen, (E, I, H), dt, H ** -0.5, pad), rows(gen, (E, I, H), dt, H ** -0.5),
+            rows(gen, (E, H, I), dt, I ** -0.5, pad))
+
+
+def f64(t):
+    return t.detach().cpu().double()
+
+
+def check(args, k, renorm, dt, lo=0, n=None):
+    x, wr, wg, wu, wd = args
+    M, H = x.shape
+    E, I = wr.shape[0], wg.shape[1]
+    n = E if n is None else n
+    y, ids, p = dgf.moe_fwd(x, wr, wg[lo:lo + n], wu[lo:lo + n], wd[lo:lo + n], k, renorm=renorm, routing=True,
+                            expert_offset=lo)
+    assert ids.shape == p.shape == (M, k) and ids.dtype == torch.int32 and p.dtype == torch.float32
+    xd, wrd = f64(x), f64(wr)
+    logits = xd @ wrd.T
+    lerr = ((H / 64 + 14) * EPS * (xd.abs() @ wrd.abs().T)).max(1, keepdim=True).values
+    got = ids.cpu().long()
+    # distinct experts, in descending order, none left out that is larger
+    assert (got >= 0).all() and (got < E).all() and all(len(set(r)) == k for r in got.tolist())
+    chosen = logits.gather(1, got)
+    assert (chosen[:, 1:] <= chosen[:, :-1] + 2 * lerr).all()
+    rest = logits.scatter(1, got, float("-inf")).max(1, keepdim=True).values
+    assert (rest <= chosen[:, -1:] + 2 * lerr).all()
+    over = chosen if renorm else logits
+    want_p = torch.exp(chosen - torch.logsumexp(over, 1, keepdim=True))
+    perr = want_p * (4 * lerr + (E / 64 + 24) * EPS)
+    assert ((f64(p) - want_p).abs() <= perr).all()
+
+    c1, c2 = 10 * (H / 64 + 1) + 16, 10 * (I / 64 + 1) + 16
+    want, size = torch.zeros(M, H, dtype=torch.float64), torch.zeros(M, H, dtype=torch.float64)
+    for m in range(M):
+        for j in range(k):
+            e = got[m, j].item()
+            if not lo <= e < lo + n:
+                continue
+            G, W, D = f64(wg[e]), f64(wu[e]), f64(wd[e])
+            g, u = G @ xd[m], W @ xd[m]
+            gs, us = G.abs() @ xd[m].abs(), W.abs() @ xd[m].abs()
+            a = g * torch.sigmoid(g) * u
+            aerr = 1.1 * c1 * EPS * (gs * u.abs() + us * g.abs()) + (KEEP[dt] + 16 * EPS) * a.abs() + 2.0 ** -26
+            want[m] += want_p[m, j] * (D @ a)
+            size[m] += want_p[m, j] * (D.abs() @ (aerr + c2 * EPS * a.abs())) + perr[m, j] * (D @ a).abs()
+    tol = U[dt] * want.abs() + size + 20 * EPS * want.abs() + 2.0 ** -25
+    off = (f64(y) - want).abs()
+    assert torch.isfinite(f64(y)).all()
+    assert (off <= tol).all(), f"{(off / tol).max():.3f} of the tolerance"
+    if want.norm() > 0:
+        assert (f64(y) - want).norm() <= U[dt] * want.norm()
+    return y, ids, p
+
+
+CASES = [(1, 64, 64, 4, 1, True), (1, 256, 128, 8, 2, True), (3, 8, 8, 3, 3, False), (5, 1003, 141, 60, 4, False),
+         (9, 129, 77, 16, 8, True), (17, 512, 96, 5, 2, True), (32, 200, 200, 128, 8, True), (4, 1, 1, 2, 1, True),
+         (64, 72, 40, 3, 1, False), (128, 136, 72, 20, 16, True), (128, 64, 64, 1, 1, True), (40, 96, 1000, 7, 7, False),
+         (2, 2048, 768, 16, 8, True), (1, 65, 3001, 9, 3, True), (7, 96, 33, 1024, 5, True)]
+
+
+@pytest.mark.parametrize("dt", [BF, FH])
+@pytest.mark.parametrize("M,H,I,E,k,renorm", CASES)
+def test_layer(M, H, I, E, k, renorm, dt):
+    check(make(M, H, I, E, dt, seed=M * H + I, pad=8 if H % 16 else 0), k, renorm, dt)
+
+
+def test_ties_go_to_the_lowest_index():
+    x, wr, wg, wu, wd = make(6, 96, 32, 200, BF)
+    wr[150], wr[70], wr[3] = wr[9], wr[9], wr[9]
+    x[2] = wr[9] * 50  # token 2 wants those four first
+    x[4] = 0           # every logit ties
+    _, ids, p = dgf.moe_fwd(x, wr, wg, wu, wd, 6, routing=True)
+    assert ids[2].tolist()[:4] == [3, 9, 70, 150]
+    assert ids[4].tolist() == [0, 1, 2, 3, 4, 5]
+    assert torch.equal(p[4], torch.full((6,), 1 / 6, dtype=torch.float32, device="cuda"))
+
+
+def test_experts_without_tokens_are_not_read():
+    # NaN and infinite weights of experts that nobody chose reach nothing
+    args = make(4, 128, 64, 32, FH, seed=3)
+    x, wr, wg, wu, wd = args
+    y, ids, _ = dgf.moe_fwd(*args, 2, routing=True)
+    idle = sorted(set(range(32)) - set(ids.flatten().tolist()))
+    assert idle
+    for e in idle:
+        wg[e], wu[e], wd[e] = float("nan"), float("inf"), float("nan")
+    assert torch.equal(dgf.moe_fwd(*args, 2), y)
+
+
+@pytest.mark.parametrize("dt", [BF, FH])
+def test_shards_of_the_experts(dt):
+    args = make(12, 192, 80, 10, dt, seed=4)
+    whole = check(args, 3, True, dt)
+    parts = [check(args, 3, True, dt, lo, n) for lo, n in ((0, 4), (4, 1), (5, 5))]
+    for y, ids, p in parts:
+        assert torch.equal(ids, whole[1]) and torch.equal(p, whole[2])
+    # each part was rounded once
+    off = (sum(f64(y) for y, *_ in parts) - f64(whole[0])).abs()
+    assert (off <= U[dt] * (sum(f64(y).abs() for y, *_ in parts) + f64(whole[0]).abs()) * 1.01 + 2.0 ** -24).all()
+    # tokens with no expert in the shard: a row of +0
+    _, ids, _ = whole
+    y = parts[1][0]
+    none = ~(ids == 4).any(1)
+    assert none.any() and (y[none].cpu().view(torch.int16) == 0).all()
+
+
+@pytest.mark.parametrize("H,I,E,k", [(512, 128, 16, 2), (192, 320, 24, 8), (100, 60, 6, 1)])
+def test_rows_do_not_depend_on_the_batch_and_runs_repeat(H, I, E, k):
+    x, *w = make(128, H, I, E, BF, seed=5)
+    full = dgf.moe_fwd(x, *w, k, routing=True)
+    again = dgf.moe_fwd(x, *w, k, routing=True)
+    for a, b in zip(full, again):
+        assert torch.equal(a, b)
+    for lo, hi in ((0, 1), (3, 4), (5, 21), (60, 128)):
+        for a, b in zip(full, dgf.moe_fwd(x[lo:hi], *w, k, routing=True)):
+            assert torch.equal(a[lo:hi], b), (lo, hi)
+
+
+def test_another_stream_and_no_tokens():
+    args = make(10, 256, 128, 8, BF, seed=6)
+    want = dgf.moe_fwd(*args, 2)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    got = dgf.moe_fwd(*args, 2, stream=side)
+    side.synchronize()
+    assert torch.equal(got, want)
+    y, ids, p = dgf.moe_fwd(args[0][:0], *args[1:], 2, routing=True)
+    assert y.shape == (0, 256) and ids.shape == (0, 2) and p.shape == (0, 2)
+
+
+def test_offsets_past_32_bits():
+    # the last expert's weights lie past 2^32 bytes (and 2^31 elements)
+    E, H, I, stride = 5, 64, 48, (1 << 29) + 8
+    args = make(6, H, I, E, BF, seed=7)
+    want = dgf.moe_fwd(*args, 2)
+
+    def far(t):
+        buf = torch.empty(stride * (E - 1) + t.shape[1] * t.shape[2], dtype=t.dtype, device="cuda")
+        v = torch.as_strided(buf, t.shape, (stride, t.shape[2], 1))
+        v.copy_(t)
+        return v
+
+    assert torch.equal(dgf.moe_fwd(args[0], args[1], far(args[2]), args[3], args[4], 2), want)
+    assert torch.equal(dgf.moe_fwd(args[0], args[1], args[2], far(args[3]), far(args[4]), 2), want)
+
+
+def test_layer_replays_from_a_hip_graph():
+    x, *w = make(16, 256, 128, 16, BF, seed=8)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        dgf.moe_fwd(x, *w, 4, routing=True)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = dgf.moe_fwd(x, *w, 4, routing=True)
+    gen = torch.Generator().manual_seed(1)
+    for i in range(4):
+        x.copy_(torch.randn(16, 256, generator=gen).to(BF))
+        graph.replay()
+        eager = dgf.moe_fwd(x.clone(), *w, 4, routing=True)
+        torch.cuda.synchronize()
+        for a, b in zip(out, eager):
+            assert torch.equal(a, b), i
