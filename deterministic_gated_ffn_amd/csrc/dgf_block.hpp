@@ -46,8 +46,9 @@ hipError_t launch_norm_bwd(const NormBwdParams &p, hipStream_t s);
 hipError_t launch_norm_wgrad(const NormBwdParams &p, hipStream_t s);
 
 // Mixture of experts (dgf_moe.hip): E experts in all, of which this call holds
-// the weights of [e0, e0 + El).  Limits: M tokens, k experts a token, E.
-constexpr int kMoeMaxM = 128, kMoeMaxK = 16, kMoeMaxE = 1024;
+// the weights of [e0, e0 + El).  Limits: M tokens, k experts a token, E, I (the
+// activations of all pairs, 4 M k I bytes, stay below 2^31).
+constexpr int kMoeMaxM = 128, kMoeMaxK = 16, kMoeMaxE = 1024, kMoeMaxI = 1 << 17;
 struct MoeParams {
   const uint16_t *x, *w_router;              // [M, H], [E, H]
   const uint16_t *w_gate, *w_up, *w_down;    // [El, I, H], [El, I, H], [El, H, I]
@@ -62,15 +63,22 @@ struct MoeParams {
   float *logits;                             // [M, E]
   float *p;                                  // [M k] routing weights
   int *ids;                                  // [M k] chosen experts
-  int *active;                               // [1 + El]: how many local experts have tokens, then which
-  int *count;                                // [El] tokens of a local expert
-  int *pairs;                                // [El, M]: its (token, choice) pairs m k + j, ascending
-  uint16_t *a_hi, *a_lo;                     // [M k, lda] the experts' activations in two parts
+  int *slots;                                // [1 + 3 min(El, M k)]: how many local experts have tokens, then of
+                                             // each its index, its first entry in `pairs` and how many it has
+  int *pairs;                                // [M k] (token, choice) pairs m k + j by slot, ascending within one
+  uint16_t *a;                               // [M k, 2 lda] the experts' activations in two parts, 8 and 8 in turn
   int64_t lda;
+  float *prod;                               // [M k, H] each pair's down product when split > 1, else null
+  int row_tiles, split;                      // of the down kernel: 8 rows each per workgroup, workgroups per row tile
 };
+// Sets row_tiles and split from the sizes.
+void moe_plan(MoeParams &p);
+// Row length of one part of `a`: I rounded up to whole steps of the down kernel.
+int64_t moe_down_ld(int I, int k);
 hipError_t launch_moe_logits(const MoeParams &p, hipStream_t s);
 hipError_t launch_moe_route(const MoeParams &p, hipStream_t s);
 hipError_t launch_moe_gate_up(const MoeParams &p, hipStream_t s);
 hipError_t launch_moe_down(const MoeParams &p, hipStream_t s);
+hipError_t launch_moe_combine(const MoeParams &p, hipStream_t s);
 
 }  // namespace dgf

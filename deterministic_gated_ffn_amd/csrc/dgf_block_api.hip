@@ -31,15 +31,16 @@ dgf_status check_norm(const void *y, const void *w_post, const void *gate, int64
 size_t carve_moe(MoeParams &p, void *ws) {
   Carve cv{(char *)ws, 0};
   const size_t pairs = (size_t)p.M * p.k;
-  p.lda = round8(p.I);
+  const size_t slots = pairs < (size_t)p.El ? pairs : (size_t)p.El;
+  p.lda = moe_down_ld(p.I, p.k);
   p.logits = (float *)cv.take((size_t)p.M * p.E * 2);
   p.p = (float *)cv.take(pairs * 2);
   p.ids = (int *)cv.take(pairs * 2);
-  p.active = (int *)cv.take((size_t)(p.El + 1) * 2);
-  p.count = (int *)cv.take((size_t)p.El * 2);
-  p.pairs = (int *)cv.take((size_t)p.El * p.M * 2);
-  p.a_hi = cv.take(pairs * p.lda);
-  p.a_lo = cv.take(pairs * p.lda);
+  p.slots = (int *)cv.take((1 + 3 * slots) * 2);
+  p.pairs = (int *)cv.take(pairs * 2);
+  p.a = cv.take(pairs * p.lda * 2);
+  moe_plan(p);
+  p.prod = p.split > 1 ? (float *)cv.take(pairs * p.H * 2) : nullptr;
   return cv.used;
 }
 
@@ -49,9 +50,9 @@ dgf_status check_moe(int64_t M, int64_t H, int64_t I, int64_t E, int64_t e0, int
   if (k < 1 || k > E) return fail(DGF_EINVAL, "k=%lld experts a token: need 1 to E=%lld", (long long)k, (long long)E);
   if (e0 < 0 || El < 1 || El > E || e0 > E - El)
     return fail(DGF_EINVAL, "experts [%lld, %lld + %lld) are not within the %lld of the router", (long long)e0, (long long)e0, (long long)El, (long long)E);
-  if (M > kMoeMaxM || k > kMoeMaxK || E > kMoeMaxE || H > kMaxLd || I > kMaxLd)
-    return fail(DGF_EUNSUPPORTED, "mixture of experts for a few tokens: M <= %d, k <= %d, E <= %d, H and I <= 2^23 (M=%lld k=%lld E=%lld)",
-                kMoeMaxM, kMoeMaxK, kMoeMaxE, (long long)M, (long long)k, (long long)E);
+  if (M > kMoeMaxM || k > kMoeMaxK || E > kMoeMaxE || I > kMoeMaxI)
+    return fail(DGF_EUNSUPPORTED, "mixture of experts for a few tokens: M <= %d, k <= %d, E <= %d, I <= %d (M=%lld k=%lld E=%lld I=%lld)",
+                kMoeMaxM, kMoeMaxK, kMoeMaxE, kMoeMaxI, (long long)M, (long long)k, (long long)E, (long long)I);
   return DGF_OK;
 }
 
@@ -221,10 +222,10 @@ dgf_status dgf_act_bwd_q8(const void *da, int64_t ldda, const void *g_q, const f
 
 size_t dgf_moe_fwd_workspace(int64_t M, int64_t H, int64_t I, int64_t E, int64_t El, int64_t k) {
   if (M <= 0 || H <= 0 || I <= 0 || E <= 0 || El <= 0 || k <= 0 || M > kMoeMaxM || E > kMoeMaxE || k > kMoeMaxK ||
-      El > E || I > kMaxLd)
+      El > E || I > kMoeMaxI)
     return 0;
   MoeParams p{};
-  p.M = (int)M; p.I = (int)I; p.E = (int)E; p.El = (int)El; p.k = (int)k;
+  p.M = (int)M; p.H = (int)H; p.I = (int)I; p.E = (int)E; p.El = (int)El; p.k = (int)k;
   return carve_moe(p, nullptr);
 }
 
@@ -263,6 +264,7 @@ dgf_status dgf_moe_fwd(const void *x, int64_t ldx, const void *w_router, int64_t
   DGF_TRY(hip_check(timed(s, "moe route", [&] { return launch_moe_route(p, s); }), "moe route"));
   DGF_TRY(hip_check(timed(s, "moe gate/up", [&] { return launch_moe_gate_up(p, s); }), "moe gate/up"));
   DGF_TRY(hip_check(timed(s, "moe down", [&] { return launch_moe_down(p, s); }), "moe down"));
+  if (p.split > 1) DGF_TRY(hip_check(timed(s, "moe combine", [&] { return launch_moe_combine(p, s); }), "moe combine"));
   return ok();
 }
 

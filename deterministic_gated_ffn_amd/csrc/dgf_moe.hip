@@ -21,6 +21,8 @@
 //
 // A token's result depends on that token alone: the K split is a function of
 // H, I and k only, sums run in a fixed order, and nothing is atomic.
+#include <math.h>
+
 #include "dgf_block.hpp"
 #include "dgf_device.hpp"
 
@@ -36,31 +38,40 @@ __device__ __forceinline__ float wave_sum(float v) {
 }
 
 // Router products, on the vector unit in FP32 (the matrix core truncates, and
-// a logit's last bits decide ties): a wave per expert and kLogitTokens tokens.
+// a logit's last bits decide ties): a workgroup per expert and kLogitTokens
+// tokens, a lane 8 of every 2048 K.
 constexpr int kLogitTokens = 4;
 
 template <class T>
 __global__ __launch_bounds__(256) void k_moe_logits(MoeParams p) {
-  const int e = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
-  if (e >= p.E) return;
+  __shared__ float red[4][kLogitTokens];
+  const int e = blockIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int m0 = blockIdx.y * kLogitTokens;
-  const uint16_t *w = p.w_router + (int64_t)e * p.ld_wr;
+  const uint16_t *w = p.w_router + e * p.ld_wr;
+  const uint16_t *x[kLogitTokens];
+#pragma unroll
+  for (int t = 0; t < kLogitTokens; ++t) x[t] = p.x + (m0 + t < p.M ? m0 + t : m0) * p.ldx;
   float acc[kLogitTokens] = {};
-  for (int c = lane * 8; c < p.H; c += 512) {
+#pragma unroll 2
+  for (int c = threadIdx.x * 8; c < p.H; c += 2048) {
     const u16x8 wv = __builtin_bit_cast(u16x8, load_frag_tail<T>(w, c, p.H));
+    u16x8 xv[kLogitTokens];
 #pragma unroll
-    for (int t = 0; t < kLogitTokens; ++t) {
-      if (m0 + t >= p.M) break;
-      const u16x8 xv = __builtin_bit_cast(u16x8, load_frag_tail<T>(p.x + (m0 + t) * p.ldx, c, p.H));
+    for (int t = 0; t < kLogitTokens; ++t) xv[t] = __builtin_bit_cast(u16x8, load_frag_tail<T>(x[t], c, p.H));
 #pragma unroll
-      for (int i = 0; i < 8; ++i) acc[t] = fmaf(T::f(wv[i]), T::f(xv[i]), acc[t]);
-    }
+    for (int t = 0; t < kLogitTokens; ++t)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc[t] = fmaf(T::f(wv[i]), T::f(xv[t][i]), acc[t]);
   }
 #pragma unroll
   for (int t = 0; t < kLogitTokens; ++t) {
     const float l = wave_sum(acc[t]);
-    if (lane == 0 && m0 + t < p.M) p.logits[(int64_t)(m0 + t) * p.E + e] = l;
+    if (lane == 0) red[wave][t] = l;
   }
+  __syncthreads();
+  const int t = threadIdx.x;
+  if (t < kLogitTokens && m0 + t < p.M)
+    p.logits[(int64_t)(m0 + t) * p.E + e] = ((red[0][t] + red[1][t]) + red[2][t]) + red[3][t];
 }
 
 // Order of logits as integers: larger float, larger integer; NaN lowest; never 0.
@@ -70,48 +81,68 @@ __device__ __forceinline__ uint32_t logit_key(float l) {
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
-// One workgroup: each wave chooses for its tokens, then lists for its experts.
+// The largest 32-bit value of the wave, uniform: shifts within rows of 16
+// lanes, then row ends broadcast (data-parallel moves, no trip through LDS).
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+  uint32_t b;
+#define DGF_MAX_STEP(ctrl, rows)                                                       \
+  b = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, ctrl, rows, 0xf, false);        \
+  v = b > v ? b : v;
+  DGF_MAX_STEP(0x111, 0xf)  // row_shr:1
+  DGF_MAX_STEP(0x112, 0xf)  // row_shr:2
+  DGF_MAX_STEP(0x114, 0xf)  // row_shr:4
+  DGF_MAX_STEP(0x118, 0xf)  // row_shr:8
+  DGF_MAX_STEP(0x142, 0xa)  // row_bcast:15
+  DGF_MAX_STEP(0x143, 0xc)  // row_bcast:31
+#undef DGF_MAX_STEP
+  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+
+// One workgroup: a wave per token chooses its experts (NL logits a lane, E <=
+// 64 NL), then a thread per expert lists its tokens.
 constexpr int kRouteThreads = 1024;
 
+template <int NL>
 __global__ __launch_bounds__(kRouteThreads) void k_moe_route(MoeParams p) {
-  __shared__ int ids[kMoeMaxM * kMoeMaxK];
-  __shared__ int cnt[kMoeMaxE];
+  __shared__ __attribute__((aligned(16))) int ids[kMoeMaxM * kMoeMaxK];
+  __shared__ int sums[kRouteThreads / 64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = kRouteThreads / 64;
+  const int n = p.M * p.k;
   for (int m = wave; m < p.M; m += waves) {
-    const float *l = p.logits + (int64_t)m * p.E;
-    float v[kMoeMaxE / 64];
-    uint32_t key[kMoeMaxE / 64];
-    float top = -INFINITY;
+    const float *l = p.logits + m * p.E;
+    float v[NL];
+    uint32_t key[NL];
 #pragma unroll
-    for (int i = 0; i < kMoeMaxE / 64; ++i) {
+    for (int i = 0; i < NL; ++i) {
       const int e = lane + 64 * i;
       v[i] = e < p.E ? l[e] : -INFINITY;
-      key[i] = e < p.E ? logit_key(v[i]) : 0u;
-      top = fmaxf(top, v[i]);
     }
 #pragma unroll
-    for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
-    float mine = -INFINITY;
+    for (int i = 0; i < NL; ++i) key[i] = lane + 64 * i < p.E ? logit_key(v[i]) : 0u;
+    float mine = -INFINITY, top = 0.0f;  // top: the first chosen, the largest
     int chosen = 0;
     for (int j = 0; j < p.k; ++j) {
-      uint64_t best = 0;
+      uint32_t best = 0;
 #pragma unroll
-      for (int i = 0; i < kMoeMaxE / 64; ++i) {
-        const uint64_t b = (uint64_t)key[i] << 32 | (uint32_t)~(lane + 64 * i);
-        if (key[i] && b > best) best = b;
+      for (int i = 0; i < NL; ++i) best = key[i] > best ? key[i] : best;
+      best = wave_max(best);
+      // the lowest index that has it, and its logit
+      int e = -1;
+      float le = 0.0f;
+#pragma unroll
+      for (int i = 0; i < NL; ++i) {
+        const uint64_t at = __ballot(key[i] == best);
+        if (e < 0 && at) {
+          const int src = __ffsll((unsigned long long)at) - 1;
+          e = 64 * i + src;
+          le = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v[i]), src));
+          if (lane == src) key[i] = 0u;
+        }
       }
-#pragma unroll
-      for (int o = 32; o > 0; o >>= 1) {
-        const uint64_t b = (uint64_t)__shfl_xor((unsigned long long)best, o);
-        best = b > best ? b : best;
-      }
-      const int e = (int)~(uint32_t)best;
-#pragma unroll
-      for (int i = 0; i < kMoeMaxE / 64; ++i)
-        if (e == lane + 64 * i) key[i] = 0u;
+      if (j == 0) top = le;
       if (lane == j) {
         chosen = e;
-        mine = l[e];
+        mine = le;
       }
     }
     float part = 0.0f;
@@ -119,7 +150,7 @@ __global__ __launch_bounds__(kRouteThreads) void k_moe_route(MoeParams p) {
       part = lane < p.k ? expf(mine - top) : 0.0f;
     } else {
 #pragma unroll
-      for (int i = 0; i < kMoeMaxE / 64; ++i)
+      for (int i = 0; i < NL; ++i)
         if (lane + 64 * i < p.E) part += expf(v[i] - top);
     }
     const float sum = wave_sum(part);
@@ -133,28 +164,40 @@ __global__ __launch_bounds__(kRouteThreads) void k_moe_route(MoeParams p) {
       if (p.p_out) p.p_out[at] = w;
     }
   }
+  if (threadIdx.x < 4 && n + (int)threadIdx.x < kMoeMaxM * kMoeMaxK) ids[n + threadIdx.x] = -1;
   __syncthreads();
-  const int n = p.M * p.k;
-  for (int e = wave; e < p.El; e += waves) {
-    int c = 0;
-    for (int b = 0; b < n; b += 64) {
-      const bool hit = b + lane < n && ids[b + lane] == p.e0 + e;
-      const uint64_t mask = __ballot(hit);
-      if (hit) p.pairs[(int64_t)e * p.M + c + __popcll(mask & ((1ull << lane) - 1))] = b + lane;
-      c += __popcll(mask);
-    }
-    if (lane == 0) cnt[e] = p.count[e] = c;
+  // thread e: local expert e's tokens; (slots << 16 | pairs) before it by a scan
+  const int want = (int)threadIdx.x < p.El ? p.e0 + (int)threadIdx.x : -2;
+  int cnt = 0;
+  for (int b = 0; b < n; b += 4) {
+    const int4 q = *reinterpret_cast<const int4 *>(&ids[b]);
+    cnt += (q.x == want) + (q.y == want) + (q.z == want) + (q.w == want);
   }
+  int scan = cnt | (cnt > 0) << 16;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int b = __shfl_up(scan, o);
+    if (lane >= o) scan += b;
+  }
+  if (lane == 63) sums[wave] = scan;
   __syncthreads();
-  if (wave == 0) {
+  int before = 0, total = 0;
+#pragma unroll
+  for (int w = 0; w < waves; ++w) {
+    before += w < wave ? sums[w] : 0;
+    total += sums[w];
+  }
+  before += scan - (cnt | (cnt > 0) << 16);
+  if (threadIdx.x == 0) p.slots[0] = total >> 16;
+  if (cnt > 0) {
+    const int start = before & 0xffff;
+    int *slot = p.slots + 1 + 3 * (before >> 16);
+    slot[0] = threadIdx.x;
+    slot[1] = start;
+    slot[2] = cnt;
     int c = 0;
-    for (int b = 0; b < p.El; b += 64) {
-      const bool hit = b + lane < p.El && cnt[b + lane] > 0;
-      const uint64_t mask = __ballot(hit);
-      if (hit) p.active[1 + c + __popcll(mask & ((1ull << lane) - 1))] = b + lane;
-      c += __popcll(mask);
-    }
-    if (lane == 0) p.active[0] = c;
+    for (int i = 0; i < n && c < cnt; ++i)
+      if (ids[i] == want) p.pairs[start + c++] = i;
   }
 }
 
@@ -167,147 +210,482 @@ __device__ __forceinline__ f32x4 diagonal(const f32x4 &acc) {
   return v;
 }
 
-template <class T>
-__device__ __forceinline__ typename T::frag zero_frag() {
-  return __builtin_bit_cast(typename T::frag, u16x8{0, 0, 0, 0, 0, 0, 0, 0});
+typedef u16x8 u16x8_any __attribute__((aligned(2)));
+
+// 8 weights, any alignment.  ONCE: their line is not asked for again, so they
+// are loaded non-temporally.  That holds where rows start on 128-byte lines
+// (the gate/up kernel at 8 of 8 experts of 12288 x 4096: 237 us against 271
+// with plain loads); elsewhere the next step needs the line's other end (20
+// experts of 1411 x 1003: 26 us against 23).
+template <class T, bool ONCE>
+__device__ __forceinline__ typename T::frag load_weights(const uint16_t *p) {
+  const u16x8_any *q = reinterpret_cast<const u16x8_any *>(p);
+  return __builtin_bit_cast(typename T::frag, ONCE ? (u16x8)__builtin_nontemporal_load(q) : (u16x8)*q);
 }
 
-// A workgroup: 8 rows of an active expert's W_gate and W_up against all its
-// tokens, 8 at a time; each wave an eighth of K.  The activation a leaves in
-// two stored parts whose sum keeps twice the stored type's bits, so that
-// rounding it adds nothing to the output's own rounding.
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+// Rows of the token operand through a buffer descriptor: a lane whose column
+// has no token gives an offset past its range and costs no memory request.
+constexpr uint32_t kNoColumn = 0x80000000u;
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t column_rsrc(const uint16_t *p, int64_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc((void *)p, (short)0, (int)bytes, 0x00020000);
+}
 template <class T>
-__global__ __launch_bounds__(64 * kWaves) void k_moe_gate_up(MoeParams p) {
-  __shared__ float red[kWaves][2][8][8];
-  if ((int)blockIdx.y >= p.active[0]) return;
-  const int e = p.active[1 + blockIdx.y], cnt = p.count[e];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+__device__ __forceinline__ typename T::frag load_column(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+  return __builtin_bit_cast(typename T::frag,
+                            __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)off, 0, 0)));
+}
+
+// A workgroup: tiles of 8 rows of an active expert's W_gate and W_up against
+// its tokens, 8 NT at a time.  `share` waves split a tile's K (whole steps of
+// 64, kChunk of them loaded together; the last of them also takes the ragged
+// rest), so that a wave has about 4 steps or more; 8 / share tiles a workgroup.
+//
+// The activation a leaves as two stored parts whose sum keeps twice the
+// stored type's bits, so that rounding it adds nothing to the output's own
+// rounding: [pair][64 of the first, 64 of the second, ...], so that a step of
+// the down kernel takes one whole line of each.  K of the down products is padded to lda with zeros, and a ragged last chunk of 8 holds its
+// values at the end, for weights read from I - 8 (see k_moe_down).
+constexpr int kChunk = 2;
+
+// First row of the tile at i0: a ragged last tile takes the last 8 rows (the
+// first of them a second time).
+__device__ __forceinline__ int tile_row(int i0, int I) { return i0 + 8 <= I || I < 8 ? i0 : I - 8; }
+
+// Where column k of a pair's row has its first part (the second: 64 further on).
+__device__ __forceinline__ int a_at(int k) { return (k >> 6) * 128 + (k & 63); }
+
+template <class T, int NT, int share, bool ONCE, bool SMALL>
+__global__ __launch_bounds__(64 * kWaves, NT == 1 ? 6 : 4) void k_moe_gate_up(MoeParams p) {
+  __shared__ __attribute__((aligned(16))) float red[kWaves][2][8 * NT][8];
+  const int n = p.slots[0], e = p.slots[1 + 3 * blockIdx.y], start = p.slots[2 + 3 * blockIdx.y],
+            cnt = p.slots[3 + 3 * blockIdx.y];
+  if ((int)blockIdx.y >= n) return;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 7, q = lane >> 4, at = ((lane >> 3) & 1) * 32 + q * 8;
-  const int i0 = blockIdx.x * 8;
-  const int row = i0 + c < p.I ? i0 + c : p.I - 1;
+  const int i0 = (blockIdx.x * kWaves + wave) / share * 8, sub = wave & (share - 1);
+  const int row = tile_row(i0, p.I) + c < p.I ? tile_row(i0, p.I) + c : p.I - 1;
   const uint16_t *wg = p.w_gate + e * p.st_wg + row * p.ld_wg;
   const uint16_t *wu = p.w_up + e * p.st_wu + row * p.ld_wu;
-  const int steps = (p.H + 63) / 64, lo = steps * wave / kWaves, hi = steps * (wave + 1) / kWaves;
-  const int *pairs = p.pairs + (int64_t)e * p.M;
-  for (int t0 = 0; t0 < cnt; t0 += 8) {
-    const bool has = t0 + c < cnt;
-    const uint16_t *x = p.x + (has ? pairs[t0 + c] / p.k : 0) * p.ldx;
-    f32x4 ag = {0.f, 0.f, 0.f, 0.f}, au = ag;
-    for (int s = lo; s < hi; ++s) {
-      const int k = s * 64 + at;
-      const typename T::frag fg = load_frag_tail<T>(wg, k, p.H), fu = load_frag_tail<T>(wu, k, p.H);
-      const typename T::frag fx = has ? load_frag_tail<T>(x, k, p.H) : zero_frag<T>();
-      ag = T::mfma(fg, fx, ag);
-      au = T::mfma(fu, fx, au);
+  const int steps = p.H / 64, lo = steps * sub / share, hi = steps * (sub + 1) / share;
+  const bool rest = sub == share - 1 && steps * 64 < p.H;
+  const __amdgpu_buffer_rsrc_t xr = column_rsrc(p.x, ((int64_t)(p.M - 1) * p.ldx + p.H) * 2);
+  for (int t0 = 0; t0 < cnt; t0 += 8 * NT) {
+    uint32_t x[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const int i = t0 + 8 * t + c;
+      x[t] = i < cnt ? (uint32_t)(p.pairs[start + i] / p.k * (int)p.ldx + at) * 2 : kNoColumn;
     }
-    const f32x4 g = diagonal(ag), u = diagonal(au);
-    if (lane < 32 && (lane & 8) == 0)
+    f32x4 ag[NT] = {}, au[NT] = {};
+    int s = lo;
+    for (; s + kChunk <= hi; s += kChunk) {
+      typename T::frag fg[kChunk], fu[kChunk], fx[kChunk][NT];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        red[wave][0][c][q * 4 + i] = g[i];
-        red[wave][1][c][q * 4 + i] = u[i];
+      for (int i = 0; i < kChunk; ++i) {
+        fg[i] = load_weights<T, ONCE>(wg + (s + i) * 64 + at);
+        fu[i] = load_weights<T, ONCE>(wu + (s + i) * 64 + at);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) fx[i][t] = load_column<T>(xr, x[t] + (s + i) * 128);
       }
-    __syncthreads();
-    if (threadIdx.x < 64) {
-      const int tok = threadIdx.x >> 3, r = threadIdx.x & 7;
-      float gs = 0.0f, us = 0.0f;
 #pragma unroll
-      for (int w = 0; w < kWaves; ++w) {
+      for (int i = 0; i < kChunk; ++i)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          ag[t] = T::mfma(fg[i], fx[i][t], ag[t]);
+          au[t] = T::mfma(fu[i], fx[i][t], au[t]);
+        }
+    }
+    for (; s < hi; ++s) {
+      const typename T::frag fg = load_weights<T, ONCE>(wg + s * 64 + at), fu = load_weights<T, ONCE>(wu + s * 64 + at);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const typename T::frag fx = load_column<T>(xr, x[t] + s * 128);
+        ag[t] = T::mfma(fg, fx, ag[t]);
+        au[t] = T::mfma(fu, fx, au[t]);
+      }
+    }
+    if (rest) {
+      // a chunk of 8 that would pass H is read from H - 8, x with zeros where
+      // the weight belongs to an earlier chunk
+      const int k = steps * 64 + at, from = k < p.H - 8 ? k : p.H - 8;
+      typename T::frag fg, fu;
+      if constexpr (SMALL) fg = load_frag_tail<T>(wg, k, p.H), fu = load_frag_tail<T>(wu, k, p.H);
+      else fg = load_weights<T, ONCE>(wg + from), fu = load_weights<T, ONCE>(wu + from);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const uint16_t *row = p.x + (x[t] < kNoColumn ? x[t] / 2 - at : 0);
+        u16x8 fx;
+        if constexpr (SMALL) {
+          fx = __builtin_bit_cast(u16x8, load_frag_tail<T>(row, k, p.H));
+        } else {
+          fx = __builtin_bit_cast(u16x8, load_weights<T, false>(row + from));
+#pragma unroll
+          for (int i = 0; i < 8; ++i) fx[i] = from + i >= k ? fx[i] : (uint16_t)0;
+        }
+        ag[t] = T::mfma(fg, __builtin_bit_cast(typename T::frag, fx), ag[t]);
+        au[t] = T::mfma(fu, __builtin_bit_cast(typename T::frag, fx), au[t]);
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const f32x4 g = diagonal(ag[t]), u = diagonal(au[t]);
+      if (lane < 32 && (lane & 8) == 0) {
+        *reinterpret_cast<f32x4 *>(&red[wave][0][8 * t + c][q * 4]) = g;
+        *reinterpret_cast<f32x4 *>(&red[wave][1][8 * t + c][q * 4]) = u;
+      }
+    }
+    __syncthreads();
+    for (int o = threadIdx.x; o < kWaves / share * 64 * NT; o += 64 * kWaves) {
+      const int w0 = o / (64 * NT) * share, tok = o / 8 % (8 * NT), r = o & 7;
+      const int ti = (blockIdx.x * kWaves + w0) / share * 8;
+      if (t0 + tok >= cnt || ti >= p.I) continue;
+      float gs = 0.0f, us = 0.0f;
+      for (int w = w0; w < w0 + share; ++w) {
         gs += red[w][0][tok][r];
         us += red[w][1][tok][r];
       }
-      if (t0 + tok < cnt && i0 + r < p.I) {
-        const float a = gs * sigma_f(gs) * us;
-        const uint16_t h = T::r(a);
-        const int64_t o = pairs[t0 + tok] * p.lda + i0 + r;
-        p.a_hi[o] = h;
-        p.a_lo[o] = T::r(a - T::f(h));
-      }
+      const int i = tile_row(ti, p.I) + r;
+      const float a = i >= ti && i < p.I ? gs * sigma_f(gs) * us : 0.0f;  // zero in a repeated row's place
+      const uint16_t h = T::r(a);
+      uint16_t *out = p.a + p.pairs[start + t0 + tok] * p.lda * 2 + r;
+      out[a_at(ti)] = h;
+      out[a_at(ti) + 64] = T::r(a - T::f(h));
+      if (ti + 8 >= p.I)  // the last tile: zeros up to lda
+        for (int k = ti + 8; k < p.lda; k += 8) out[a_at(k)] = out[a_at(k) + 64] = 0;
     }
     __syncthreads();
   }
 }
 
-// A workgroup: 8 rows of y.  Its waves work in groups of `wps`, a group on one
-// active expert at a time, each wave of it a share of K = I; wps is 8 / k
-// (down to a power of two), so that the experts of a single token keep all
-// waves busy.  Each (token, choice) pair's partial products are kept in LDS
-// and added up in order at the end: the waves' shares, then the choices by p.
-template <class T>
+// A workgroup: 8 RT rows of y over all active experts.  Its waves work in groups
+// of `wps`, a group on one expert at a time, each wave of it a share of K = I;
+// wps is 8 / k (down to a power of two), so that the experts of a single token
+// keep all waves busy.  A wave's steps (64 K of an expert's rows against 8 NT
+// of its tokens) form one stream over all its experts, and the loads run R
+// steps ahead of the products through it: 8 R RT KB of weights in flight per
+// workgroup.  Loads past the end of the stream
+// read one fixed line.
+//
+// The weights' last ragged chunk of 8 is read from I - 8, against a's last
+// chunk with its values at the end and zeros before, and later chunks again
+// from there against zeros: no load passes a row's end.  (SMALL: I < 8, where
+// there is no such 8; element by element.)
+//
+// Each (token, choice) pair's partial products stay in LDS and are added up in
+// order at the end: the waves' shares, then the choices by p.  Where the rows
+// of y alone make too few workgroups, grid.y workgroups share the experts of a
+// row tile: the products of a pair then go to `prod` and k_moe_combine weighs
+// and adds them, the same operations in the same order.
+struct MoeSlot {
+  int e, start, cnt;
+};
+constexpr float kNotHere = -1.0f;  // in place of a routing weight (never negative): another call has that expert
+
+template <class T, int RT, int NT, int R, bool ONCE, bool SMALL>
 __global__ __launch_bounds__(64 * kWaves) void k_moe_down(MoeParams p, int wps) {
-  extern __shared__ float part[];  // [M k][wps][8 rows]
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  constexpr int ROWS = 8 * RT;
+  extern __shared__ __attribute__((aligned(16))) float part[];  // [M k][wps][ROWS]
+  const int np = p.M * p.k, ns = np < p.El ? np : p.El;
+  int *pairs = reinterpret_cast<int *>(part + np * wps * ROWS);
+  MoeSlot *slots = reinterpret_cast<MoeSlot *>(pairs + np);
+  for (int i = threadIdx.x; i < np; i += 64 * kWaves) pairs[i] = p.pairs[i];
+  float *weight = reinterpret_cast<float *>(slots + ns);  // p, or kNotHere
+  for (int i = threadIdx.x; i < 3 * ns; i += 64 * kWaves) reinterpret_cast<int *>(slots)[i] = p.slots[1 + i];
+  if (!p.prod)
+    for (int i = threadIdx.x; i < np; i += 64 * kWaves) {
+      const int e = p.ids[i] - p.e0;
+      const float w = p.p[i];
+      weight[i] = e >= 0 && e < p.El ? w : kNotHere;
+    }
+  const int n = p.slots[0];
+  __syncthreads();
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 7, q = lane >> 4, at = ((lane >> 3) & 1) * 32 + q * 8;
-  const int h0 = blockIdx.x * 8;
-  const int row = h0 + c < p.H ? h0 + c : p.H - 1;
-  const int sub = wave & (wps - 1), groups = kWaves / wps;
-  const int steps = (p.I + 63) / 64, lo = steps * sub / wps, hi = steps * (sub + 1) / wps;
-  const int n = p.active[0];
-  for (int s0 = wave / wps; s0 < n; s0 += groups) {
-    const int e = p.active[1 + s0], cnt = p.count[e];
-    const uint16_t *w = p.w_down + e * p.st_wd + row * p.ld_wd;
-    const int *pairs = p.pairs + (int64_t)e * p.M;
-    for (int t0 = 0; t0 < cnt; t0 += 8) {
-      const bool has = t0 + c < cnt;
-      const int pair = has ? pairs[t0 + c] : 0;
-      const uint16_t *ah = p.a_hi + pair * p.lda, *al = p.a_lo + pair * p.lda;
-      f32x4 acc = {0.f, 0.f, 0.f, 0.f}, acl = acc;
-      for (int s = lo; s < hi; ++s) {
-        const int k = s * 64 + at;
-        const typename T::frag fw = load_frag_tail<T>(w, k, p.I);
-        acc = T::mfma(fw, has ? load_frag_tail<T>(ah, k, p.I) : zero_frag<T>(), acc);
-        acl = T::mfma(fw, has ? load_frag_tail<T>(al, k, p.I) : zero_frag<T>(), acl);
+  const int h0 = blockIdx.x * ROWS;
+  const int sub = wave & (wps - 1), groups = kWaves / wps * (int)gridDim.y;
+  const int len = (int)(p.lda / (64 * wps)), k0 = sub * len * 64 + at;  // this wave's steps of an expert, its first column
+  const uint16_t *wrow[RT];
+#pragma unroll
+  for (int i = 0; i < RT; ++i) wrow[i] = p.w_down + (h0 + 8 * i + c < p.H ? h0 + 8 * i + c : p.H - 1) * p.ld_wd;
+
+  struct Step {
+    typename T::frag w[RT], hi[NT], lo[NT];
+  };
+  struct Cursor {
+    int slot, t0, step, cnt, start, e;
+  };
+  auto open = [&](Cursor &u) {
+    const MoeSlot v = slots[u.slot < n ? u.slot : 0];
+    u.e = __builtin_amdgcn_readfirstlane(v.e);
+    u.start = __builtin_amdgcn_readfirstlane(v.start);
+    u.cnt = __builtin_amdgcn_readfirstlane(v.cnt);
+  };
+  Cursor ld = {wave / wps * (int)gridDim.y + (int)blockIdx.y, 0, 0, 0, 0, 0};
+  const uint16_t *w[RT];
+  uint32_t a[NT];
+  int go = 1;  // steps that a load advances: 0 past the end of the stream
+  const __amdgpu_buffer_rsrc_t ar = column_rsrc(p.a, np * p.lda * 4);
+  auto point = [&] {  // the cursor's expert and tokens
+#pragma unroll
+    for (int i = 0; i < RT; ++i) w[i] = wrow[i] + ld.e * p.st_wd;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const int i = ld.t0 + 8 * t + c;
+      a[t] = i < ld.cnt ? (uint32_t)((pairs[ld.start + i] * (int)p.lda + k0 - at) * 2 + at) * 2 : kNoColumn;
+    }
+  };
+  auto load = [&](Step &v) {  // no branch around the loads: the compiler then counts them exactly
+    const int k = k0 + ld.step * 64;
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+      if constexpr (SMALL) v.w[i] = load_frag_tail<T>(w[i], k, p.I);
+      else v.w[i] = load_weights<T, ONCE>(w[i] + (k < p.I - 8 ? k : p.I - 8));
+    }
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      v.hi[t] = load_column<T>(ar, a[t] + ld.step * 256);
+      v.lo[t] = load_column<T>(ar, a[t] + ld.step * 256 + 128);
+    }
+    ld.step += go;
+    if (ld.step < len) return;
+    ld.step = 0;
+    ld.t0 += 8 * NT;
+    if (ld.t0 >= ld.cnt) {
+      ld.t0 = 0;
+      ld.slot += groups;
+      open(ld);
+    }
+    if (ld.slot < n) {
+      point();
+    } else {
+      go = 0;
+#pragma unroll
+      for (int i = 0; i < RT; ++i) w[i] = p.w_down;
+#pragma unroll
+      for (int t = 0; t < NT; ++t) a[t] = kNoColumn;
+    }
+  };
+
+  if (ld.slot < n) {
+    Cursor cu = ld;
+    open(ld);
+    open(cu);
+    point();
+    Step ring[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) load(ring[r]);
+    f32x4 acc[RT][NT] = {};
+    while (cu.slot < n) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        if (cu.slot < n) {
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int i = 0; i < RT; ++i) {
+              acc[i][t] = T::mfma(ring[r].w[i], ring[r].hi[t], acc[i][t]);
+              acc[i][t] = T::mfma(ring[r].w[i], ring[r].lo[t], acc[i][t]);
+            }
+          if (++cu.step == len) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+              const int at_ = cu.t0 + 8 * t + c;
+#pragma unroll
+              for (int i = 0; i < RT; ++i) {
+                const f32x4 v = diagonal(acc[i][t]);
+                if (lane < 32 && (lane & 8) == 0 && at_ < cu.cnt)
+                  *reinterpret_cast<f32x4 *>(&part[(pairs[cu.start + at_] * wps + sub) * ROWS + 8 * i + q * 4]) = v;
+                acc[i][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+              }
+            }
+            cu.step = 0;
+            cu.t0 += 8 * NT;
+            if (cu.t0 >= cu.cnt) {
+              cu.t0 = 0;
+              cu.slot += groups;
+              open(cu);
+            }
+          }
+        }
+        load(ring[r]);
       }
-      const f32x4 v = diagonal(acc + acl);
-      if (lane < 32 && (lane & 8) == 0 && has)
-        *reinterpret_cast<f32x4 *>(&part[(pair * wps + sub) * 8 + q * 4]) = v;
     }
   }
   __syncthreads();
-  for (int o = threadIdx.x; o < p.M * 8; o += 64 * kWaves) {
-    const int m = o >> 3, r = o & 7;
+  if (p.prod) {
+    for (int s = wave * (int)gridDim.y + (int)blockIdx.y; s < n; s += kWaves * (int)gridDim.y)
+      for (int o = lane; o < slots[s].cnt * ROWS; o += 64) {
+        const int pair = pairs[slots[s].start + o / ROWS], r = o % ROWS;
+        float t = 0.0f;
+        for (int i = 0; i < wps; ++i) t += part[(pair * wps + i) * ROWS + r];
+        if (h0 + r < p.H) p.prod[(int64_t)pair * p.H + h0 + r] = t;
+      }
+    return;
+  }
+  for (int o = threadIdx.x; o < p.M * ROWS; o += 64 * kWaves) {
+    const int m = o / ROWS, r = o % ROWS;
     if (h0 + r >= p.H) continue;
     float y = 0.0f;
     for (int j = 0; j < p.k; ++j) {
-      const int e = p.ids[m * p.k + j] - p.e0;
-      if (e < 0 || e >= p.El) continue;
+      const float w = weight[m * p.k + j];
+      if (w == kNotHere) continue;
       float t = 0.0f;
-      for (int w = 0; w < wps; ++w) t += part[((m * p.k + j) * wps + w) * 8 + r];
-      y = fmaf(p.p[m * p.k + j], t, y);
+      for (int i = 0; i < wps; ++i) t += part[((m * p.k + j) * wps + i) * ROWS + r];
+      y = fmaf(w, t, y);
     }
     p.y[m * p.ldy + h0 + r] = T::r(y);
   }
 }
 
+template <class T>
+__global__ __launch_bounds__(256) void k_moe_combine(MoeParams p) {
+  const int h = blockIdx.x * 256 + threadIdx.x, m = blockIdx.y;
+  if (h >= p.H) return;
+  float y = 0.0f;
+#pragma unroll 4
+  for (int j = 0; j < p.k; ++j) {
+    const int e = p.ids[m * p.k + j] - p.e0;
+    const bool local = e >= 0 && e < p.El;  // prod holds nothing for the others
+    const float t = local ? p.prod[(int64_t)(m * p.k + j) * p.H + h] : 0.0f;
+    y = local ? fmaf(p.p[m * p.k + j], t, y) : y;
+  }
+  p.y[m * p.ldy + h] = T::r(y);
+}
+
+// Waves that share an expert in the down kernel.
+int waves_per_slot(int k) {
+  int wps = 1;
+  while (wps * 2 * k <= kWaves) wps *= 2;
+  return wps;
+}
+
+// What a CU reads (about 27 GB/s of it) in the time that the combining launch
+// takes, and in a workgroup's start and end.
+constexpr double kCombineBytes = 100e3, kStartBytes = 60e3;
+
+// Token tiles of 8 that one pass over an expert's weights takes, from the
+// mean number of tokens an expert gets.
+int token_tiles(const MoeParams &p) {
+  const int64_t pairs = (int64_t)p.M * p.k;
+  return pairs <= 4 * (int64_t)p.E ? 1 : pairs <= 12 * (int64_t)p.E ? 2 : 4;
+}
+
+// Whether every row of an expert matrix starts on a 128-byte line.
+bool line_rows(const uint16_t *w, int64_t ld, int64_t stride) {
+  return ((uintptr_t)w & 127) == 0 && ld % 64 == 0 && stride % 64 == 0;
+}
+
+template <class T, int SHARE>
+hipError_t gate_up_s(const MoeParams &p, hipStream_t s) {
+  constexpr int rows = 8 * (kWaves / SHARE);
+  const int slots = p.M * p.k < p.El ? p.M * p.k : p.El;  // at most this many experts have tokens
+  const dim3 g((p.I + rows - 1) / rows, slots), b(64 * kWaves);
+  const bool once = line_rows(p.w_gate, p.ld_wg, p.st_wg) && line_rows(p.w_up, p.ld_wu, p.st_wu);
+  switch (token_tiles(p) * 2 + once) {
+    case 2: dgf_launch((k_moe_gate_up<T, 1, SHARE, false, false>), g, b, 0, s, p); break;
+    case 3: dgf_launch((k_moe_gate_up<T, 1, SHARE, true, false>), g, b, 0, s, p); break;
+    case 4: dgf_launch((k_moe_gate_up<T, 2, SHARE, false, false>), g, b, 0, s, p); break;
+    case 5: dgf_launch((k_moe_gate_up<T, 2, SHARE, true, false>), g, b, 0, s, p); break;
+    case 8: dgf_launch((k_moe_gate_up<T, 4, SHARE, false, false>), g, b, 0, s, p); break;
+    default: dgf_launch((k_moe_gate_up<T, 4, SHARE, true, false>), g, b, 0, s, p); break;
+  }
+  return hipGetLastError();
+}
+
+// Waves that split a tile's K: 4 steps of 64 or more each.
+template <class T>
+hipError_t gate_up_t(const MoeParams &p, hipStream_t s) {
+  if (p.H < 8) {
+    const dim3 g((p.I + 63) / 64, p.M * p.k < p.El ? p.M * p.k : p.El);
+    dgf_launch((k_moe_gate_up<T, 1, 1, false, true>), g, dim3(64 * kWaves), 0, s, p);
+    return hipGetLastError();
+  }
+  const int steps = p.H / 64;
+  return steps >= 32 ? gate_up_s<T, 8>(p, s) : steps >= 16 ? gate_up_s<T, 4>(p, s) : steps >= 8 ? gate_up_s<T, 2>(p, s) : gate_up_s<T, 1>(p, s);
+}
+
+template <class T, int RT>
+hipError_t down_rt(const MoeParams &p, hipStream_t s) {
+  const int wps = waves_per_slot(p.k), np = p.M * p.k, slots = np < p.El ? np : p.El;
+  const dim3 g((p.H + 8 * RT - 1) / (8 * RT), p.split), b(64 * kWaves);
+  // at most 64 RT KB of partial products (M k wps <= 2048), 16 of pairs and their weights, 12 of slots: 156 of 160
+  const size_t lds = (size_t)np * wps * 8 * RT * 4 + (size_t)np * 8 + (size_t)slots * sizeof(MoeSlot);
+  if (p.I < 8) dgf_launch((k_moe_down<T, RT, 1, 2, false, true>), g, b, lds, s, p, wps);
+  else switch (token_tiles(p) * 2 + line_rows(p.w_down, p.ld_wd, p.st_wd)) {
+    case 2: dgf_launch((k_moe_down<T, RT, 1, 8, false, false>), g, b, lds, s, p, wps); break;
+    case 3: dgf_launch((k_moe_down<T, RT, 1, 8, true, false>), g, b, lds, s, p, wps); break;
+    case 4: dgf_launch((k_moe_down<T, RT, 2, 6, false, false>), g, b, lds, s, p, wps); break;
+    case 5: dgf_launch((k_moe_down<T, RT, 2, 6, true, false>), g, b, lds, s, p, wps); break;
+    case 8: dgf_launch((k_moe_down<T, RT, 4, 4, false, false>), g, b, lds, s, p, wps); break;
+    default: dgf_launch((k_moe_down<T, RT, 4, 4, true, false>), g, b, lds, s, p, wps); break;
+  }
+  return hipGetLastError();
+}
+
+template <class T>
+hipError_t down_t(const MoeParams &p, hipStream_t s) {
+  return p.row_tiles == 2 ? down_rt<T, 2>(p, s) : down_rt<T, 1>(p, s);
+}
+
 }  // namespace
 
+// Row tiles a workgroup and workgroups a row tile, by the bytes that pass
+// through the busiest CU: its waves' weights, in whole rounds of experts, and
+// its pairs' activations (from L2, at three quarters of the cost), for every
+// round of workgroups; sharing out the experts costs the combining launch.
+void moe_plan(MoeParams &p) {
+  const int wps = waves_per_slot(p.k), groups = kWaves / wps;
+  const double pairs = (double)p.M * p.k * p.El / p.E;
+  const double slots = p.El * (1.0 - pow(1.0 - (double)p.k / p.E, p.M));  // experts with tokens, on average
+  double best = 0.0;
+  for (int rt = 1; rt <= 2; ++rt) {
+    const int tiles = (p.H + 8 * rt - 1) / (8 * rt);
+    for (int z = 1; z <= 32 && (z == 1 || (z - 1) * groups < slots); ++z) {
+      // a last round that only some waves have leaves the others' bandwidth to them: count it half
+      const double exact = slots / (z * groups), rounds = 0.5 * (exact + ceil(exact));
+      const double wg = rounds * kWaves * 8.0 * rt * 2.0 * p.I / wps + 0.75 * pairs / z * p.I * 4.0;
+      const double cost = ceil(tiles * z / 256.0) * (wg + kStartBytes) + (z > 1 ? kCombineBytes : 0.0);
+      if (best == 0.0 || cost < best) {
+        best = cost;
+        p.row_tiles = rt;
+        p.split = z;
+      }
+    }
+  }
+}
+
+int64_t moe_down_ld(int I, int k) {
+  const int step = 64 * waves_per_slot(k);
+  return (int64_t)(I + step - 1) / step * step;
+}
+
 hipError_t launch_moe_logits(const MoeParams &p, hipStream_t s) {
-  const dim3 g((p.E + 3) / 4, (p.M + kLogitTokens - 1) / kLogitTokens);
+  const dim3 g(p.E, (p.M + kLogitTokens - 1) / kLogitTokens);
   if (p.fmt == FMT_F16) dgf_launch(k_moe_logits<F16>, g, dim3(256), 0, s, p);
   else dgf_launch(k_moe_logits<Bf16>, g, dim3(256), 0, s, p);
   return hipGetLastError();
 }
 
 hipError_t launch_moe_route(const MoeParams &p, hipStream_t s) {
-  dgf_launch(k_moe_route, dim3(1), dim3(kRouteThreads), 0, s, p);
+  if (p.E <= 128) dgf_launch(k_moe_route<2>, dim3(1), dim3(kRouteThreads), 0, s, p);
+  else dgf_launch(k_moe_route<kMoeMaxE / 64>, dim3(1), dim3(kRouteThreads), 0, s, p);
   return hipGetLastError();
 }
 
 hipError_t launch_moe_gate_up(const MoeParams &p, hipStream_t s) {
-  const int slots = p.M * p.k < p.El ? p.M * p.k : p.El;  // at most this many experts have tokens
-  const dim3 g((p.I + 7) / 8, slots);
-  if (p.fmt == FMT_F16) dgf_launch(k_moe_gate_up<F16>, g, dim3(64 * kWaves), 0, s, p);
-  else dgf_launch(k_moe_gate_up<Bf16>, g, dim3(64 * kWaves), 0, s, p);
-  return hipGetLastError();
+  return p.fmt == FMT_F16 ? gate_up_t<F16>(p, s) : gate_up_t<Bf16>(p, s);
 }
 
 hipError_t launch_moe_down(const MoeParams &p, hipStream_t s) {
-  int wps = 1;
-  while (wps * 2 * p.k <= kWaves) wps *= 2;
-  const dim3 g((p.H + 7) / 8);
-  const size_t lds = (size_t)p.M * p.k * wps * 8 * 4;  // at most 64 KB: M k wps <= 2048
-  if (p.fmt == FMT_F16) dgf_launch(k_moe_down<F16>, g, dim3(64 * kWaves), lds, s, p, wps);
-  else dgf_launch(k_moe_down<Bf16>, g, dim3(64 * kWaves), lds, s, p, wps);
+  return p.fmt == FMT_F16 ? down_t<F16>(p, s) : down_t<Bf16>(p, s);
+}
+
+hipError_t launch_moe_combine(const MoeParams &p, hipStream_t s) {
+  const dim3 g((p.H + 255) / 256, p.M);
+  if (p.fmt == FMT_F16) dgf_launch(k_moe_combine<F16>, g, dim3(256), 0, s, p);
+  else dgf_launch(k_moe_combine<Bf16>, g, dim3(256), 0, s, p);
   return hipGetLastError();
 }
 

@@ -328,7 +328,7 @@ dgf_status dgf_ffn_bwd_q8(const void *dy, int64_t lddy, const void *x, int64_t l
  * twice the stored type's bits); y is rounded once.  Row m of every output
  * depends on row m of x only, bit for bit, whatever M is, so more than 128
  * tokens can be given in pieces.
- * Limits: M <= 128, k <= 16, E <= 1024 (else DGF_EUNSUPPORTED).  Workspace:
+ * Limits: M <= 128, k <= 16, E <= 1024, I <= 131072 (else DGF_EUNSUPPORTED).  Workspace:
  * dgf_moe_fwd_workspace bytes.  M = 0: DGF_OK, no launch.
  */
 size_t dgf_moe_fwd_workspace(int64_t M, int64_t H, int64_t I, int64_t E, int64_t El, int64_t k);
