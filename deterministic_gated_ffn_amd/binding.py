@@ -106,8 +106,8 @@ def _check(status: int, where: str):
 
 
 def _stream(stream=None) -> int:
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:  # the handle alone: building a Stream object costs a small call's kernel time
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream
 
 
@@ -148,8 +148,8 @@ def _mat(t: torch.Tensor, name: str):
 def _empty(rows: int, cols: int, like: torch.Tensor, ld: int | None = None) -> torch.Tensor:
     """Row-major [rows, cols] of like's dtype whose leading dimension is a multiple of 8."""
     ld = ld or ((cols + 7) // 8) * 8
-    buf = torch.empty((rows, ld), dtype=like.dtype, device=like.device)
-    return buf[:, :cols]
+    buf = like.new_empty((rows, ld))
+    return buf if ld == cols else buf[:, :cols]
 
 
 def _workspace(nbytes: int, like: torch.Tensor) -> torch.Tensor:

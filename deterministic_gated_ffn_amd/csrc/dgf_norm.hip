@@ -4,54 +4,69 @@
 //   z = alpha res + gate t                               (the new residual stream)
 //   h = z r_z w_next,  r_z = 1/sqrt(mean(z^2) + eps)     (the next block's input)
 //
-// One workgroup per row, the row in its registers: y and res are read once,
-// z and h written once, 8 bytes an element against about 12 operations, so
-// the kernels are bound by HBM.  Everything between the loads and the stores
-// is FP32; z and h are each rounded once, h from the unrounded z.
+// A row lives in the registers of its threads: y and res are read once, z and h
+// written once, 8 bytes an element against about 12 operations, so the kernels
+// are bound by HBM.  Everything between the loads and the stores is FP32; z and
+// h are each rounded once, h from the unrounded z.
 #include "dgf_block.hpp"
 #include "dgf_rows.hpp"
 
 namespace dgf {
 namespace {
 
-// Sums of N values over the workgroup, the same bits in every thread: a
-// butterfly within each wave, then the waves in order.  red holds 16 N floats
-// that no other reduction of this row uses.
+constexpr int kBwdThreads = 512;
+
+// Sums of N <= 4 values over the waves [w0, w0 + waves) of the workgroup that
+// share a row, the same bits in all their threads: within each wave, then the
+// waves in order.  red: one float4 a wave, not used by the row before or after.
 template <int N>
-__device__ __forceinline__ void row_sums(float (&v)[N], float *red) {
+__device__ __forceinline__ void row_sums(float (&v)[N], float4 *red, int w0, int waves) {
 #pragma unroll
-  for (int o = 32; o > 0; o >>= 1)
+  for (int i = 0; i < N; ++i) v[i] = wave_sum_last(v[i]);
+  if ((threadIdx.x & 63) == 63) {
+    float f[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] += __shfl_xor(v[i], o);
-  const int waves = blockDim.x >> 6;
-  if (waves == 1) return;
-  if ((threadIdx.x & 63) == 0)
-#pragma unroll
-    for (int i = 0; i < N; ++i) red[i * 16 + (threadIdx.x >> 6)] = v[i];
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    float t = red[i * 16];
-    for (int w = 1; w < waves; ++w) t += red[i * 16 + w];
-    v[i] = t;
+    for (int i = 0; i < N; ++i) f[i] = v[i];
+    red[threadIdx.x >> 6] = make_float4(f[0], f[1], f[2], f[3]);
   }
+  __syncthreads();
+  float4 t = red[w0];
+#pragma unroll 4
+  for (int w = 1; w < waves; ++w) {
+    const float4 q = red[w0 + w];
+    t.x += q.x; t.y += q.y; t.z += q.z; t.w += q.w;
+  }
+  const float f[4] = {t.x, t.y, t.z, t.w};
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = f[i];
 }
 
-template <class T, int V>
+// One workgroup per row; everything it reads is asked for before the first sum.
+template <class T, int V, bool WHOLE>
 __global__ __launch_bounds__(1024) void k_norm_fwd(NormFwdParams p) {
-  __shared__ float red[2][16];
+  __shared__ float4 red[2][16];
   const int64_t m = blockIdx.x;
-  const int H = (int)p.H;
+  const int H = (int)p.H, waves = blockDim.x >> 6;
   const float inv_h = 1.0f / (float)H;
-  uint4 yv[V], rv[V];
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  auto ld = [&](const uint16_t *row, int c) {
+    return WHOLE ? *reinterpret_cast<const uint4 *>(row + c) : row_ld(row, c, H);
+  };
+  auto st = [&](uint16_t *row, int c, const uint4 &v) {
+    if constexpr (WHOLE) *reinterpret_cast<uint4 *>(row + c) = v;
+    else row_st(row, c, H, v);
+  };
+  uint4 yv[V], rv[V], wp[V], wg[V], wn[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     const int c = (threadIdx.x + v * blockDim.x) * 8;
-    rv[v] = yv[v] = make_uint4(0, 0, 0, 0);
-    if (c < H) {
-      rv[v] = row_ld(p.res + m * p.ld_res, c, H);
-      if (p.y) yv[v] = row_ld(p.y + m * p.ld_y, c, H);
-    }
+    rv[v] = yv[v] = wp[v] = wg[v] = wn[v] = zero;
+    if (c >= H) continue;
+    if (p.y) yv[v] = ld(p.y + m * p.ld_y, c);
+    rv[v] = ld(p.res + m * p.ld_res, c);
+    if (p.w_post) wp[v] = ld(p.w_post, c);
+    if (p.gate) wg[v] = ld(p.gate + m * p.ld_gate, c);
+    if (p.w_next) wn[v] = ld(p.w_next, c);
   }
   float r_y = 1.0f;
   if (p.w_post) {
@@ -63,7 +78,7 @@ __global__ __launch_bounds__(1024) void k_norm_fwd(NormFwdParams p) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) s[0] = fmaf(y[e], y[e], s[0]);
     }
-    row_sums(s, red[0]);
+    row_sums(s, red[0], 0, waves);
     r_y = 1.0f / sqrtf(fmaf(s[0], inv_h, p.eps));
   }
   float z[V][8];
@@ -76,35 +91,35 @@ __global__ __launch_bounds__(1024) void k_norm_fwd(NormFwdParams p) {
       float t[8], f[8];
       row_widen<T>(yv[v], t);
       if (p.w_post) {
-        row_widen<T>(row_ld(p.w_post, c, H), f);
+        row_widen<T>(wp[v], f);
 #pragma unroll
         for (int e = 0; e < 8; ++e) t[e] = t[e] * r_y * f[e];
       }
       if (p.gate) {
-        row_widen<T>(row_ld(p.gate + m * p.ld_gate, c, H), f);
+        row_widen<T>(wg[v], f);
 #pragma unroll
         for (int e = 0; e < 8; ++e) t[e] *= f[e];
       }
 #pragma unroll
       for (int e = 0; e < 8; ++e) z[v][e] = fmaf(p.alpha, z[v][e], t[e]);
-      row_st(p.z + m * p.ld_z, c, H, row_narrow<T>(z[v]));
+      st(p.z + m * p.ld_z, c, row_narrow<T>(z[v]));
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e) s[0] = fmaf(z[v][e], z[v][e], s[0]);
   }
   float r_z = 1.0f;
   if (p.w_next) {
-    row_sums(s, red[1]);
+    row_sums(s, red[1], 0, waves);
     r_z = 1.0f / sqrtf(fmaf(s[0], inv_h, p.eps));
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int c = (threadIdx.x + v * blockDim.x) * 8;
       if (c >= H) continue;
       float f[8];
-      row_widen<T>(row_ld(p.w_next, c, H), f);
+      row_widen<T>(wn[v], f);
 #pragma unroll
       for (int e = 0; e < 8; ++e) f[e] *= z[v][e] * r_z;
-      row_st(p.h + m * p.ld_h, c, H, row_narrow<T>(f));
+      st(p.h + m * p.ld_h, c, row_narrow<T>(f));
     }
   }
   if (p.rstd && threadIdx.x == 0) {
@@ -113,7 +128,8 @@ __global__ __launch_bounds__(1024) void k_norm_fwd(NormFwdParams p) {
   }
 }
 
-// The backward, each workgroup over its own rows m = blockIdx.x, + groups, ...
+// The backward.  A workgroup holds blockDim / row_threads rows at a time, and
+// goes over its own rows in steps of the whole grid's.
 //
 //   G  = dz + r_z (dn - z r_z^2 mean(dn z)),  dn = dh w_next
 //   dres = alpha G,  dgate = G t,  dq = G gate w_post,
@@ -123,54 +139,111 @@ __global__ __launch_bounds__(1024) void k_norm_fwd(NormFwdParams p) {
 // sum first: with q = gate w_post y, sum(G q) = sum((dz + r_z dn) q) - c sum(z q),
 // c = r_z^3 mean(dn z).  All three sums of a row take one reduction.  The
 // column sums dw_post, dw_next and a broadcast dgate stay in registers over
-// the workgroup's rows and go to `part` once (FP32, added up by k_norm_wgrad
-// in the order of the workgroups, so results do not change from run to run).
-template <class T, int V>
-__global__ __launch_bounds__(1024) void k_norm_bwd(NormBwdParams p) {
-  __shared__ float red[2][3][16];
+// the workgroup's rows, then its row slots add up through LDS, in order, and
+// go to `part` once (FP32, added up by k_norm_wgrad in the order of the
+// workgroups, so results do not change from run to run).
+//
+// ALL: dz, dh, y and w_post are all given (no test of them in the loop).  It
+// loads the next row before this one's reduction for rows of up to 8192
+// (V <= 2); wider ones have no registers left for that.  WHOLE: H is a multiple
+// of 8 (no element-by-element ends, which cost registers too).
+enum { GATE_NONE = 0, GATE_ROW = 1, GATE_FULL = 2 };
+
+template <int V, int GATE>
+struct NormRow {
+  uint4 dz[V], dh[V], z[V], y[V], gate[GATE == GATE_FULL ? V : 1];
+  float r_y, r_z;
+};
+
+template <class T, int V, int GATE, bool ALL, bool WHOLE>
+__global__ __launch_bounds__(kBwdThreads, V == 1 ? 4 : 2) void k_norm_bwd(NormBwdParams p, int row_threads) {
+  __shared__ float4 red[2][kBwdThreads / 64];
+  extern __shared__ float cols[];  // round8(H) column sums, when a workgroup holds several rows
+  constexpr bool AHEAD = ALL && V <= 2;
   const int H = (int)p.H;
   const float inv_h = 1.0f / (float)H;
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  const bool has_dz = ALL || p.dz, has_dh = ALL || p.dh, has_y = ALL || p.y, has_post = ALL || p.w_post;
+  const int slots = blockDim.x / row_threads, slot = __builtin_amdgcn_readfirstlane(threadIdx.x / row_threads);
+  const int tid = threadIdx.x - slot * row_threads;
+  const int w0 = slot * (row_threads >> 6), waves = row_threads >> 6;
+  auto ld = [&](const uint16_t *row, int c) {
+    return WHOLE ? *reinterpret_cast<const uint4 *>(row + c) : row_ld(row, c, H);
+  };
+  auto st = [&](uint16_t *row, int c, const uint4 &v) {
+    if constexpr (WHOLE) *reinterpret_cast<uint4 *>(row + c) = v;
+    else row_st(row, c, H, v);
+  };
+  auto col = [&](int v) { return (tid + v * row_threads) * 8; };
   float ap[V][8] = {}, an[V][8] = {}, ag[V][8] = {};
-  int turn = 0;
-  for (int64_t m = blockIdx.x; m < p.M; m += gridDim.x, turn ^= 1) {
-    uint4 gv[V], dv[V], zv[V], yv[V];
+  uint4 wp[V], wn[V], wg[V];  // w_post, w_next and a broadcast gate
+  auto load = [&](int64_t m, NormRow<V, GATE> &r) {
+    r.r_y = p.rstd[2 * m];
+    r.r_z = p.rstd[2 * m + 1];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int c = (threadIdx.x + v * blockDim.x) * 8;
-      gv[v] = dv[v] = zv[v] = yv[v] = make_uint4(0, 0, 0, 0);
-      if (c < H) {
-        if (p.dz) gv[v] = row_ld(p.dz + m * p.ld_dz, c, H);
-        if (p.dh) dv[v] = row_ld(p.dh + m * p.ld_dh, c, H), zv[v] = row_ld(p.z + m * p.ld_z, c, H);
-        if (p.y) yv[v] = row_ld(p.y + m * p.ld_y, c, H);
+      const int c = col(v);
+      r.dz[v] = r.dh[v] = r.z[v] = r.y[v] = zero;
+      if constexpr (GATE == GATE_FULL) r.gate[v] = zero;
+      if (c >= H) continue;
+      if (has_dz) r.dz[v] = ld(p.dz + m * p.ld_dz, c);
+      if (has_dh) {
+        r.dh[v] = ld(p.dh + m * p.ld_dh, c);
+        r.z[v] = ld(p.z + m * p.ld_z, c);
       }
+      if (has_y) r.y[v] = ld(p.y + m * p.ld_y, c);
+      if constexpr (GATE == GATE_FULL) r.gate[v] = ld(p.gate + m * p.ld_gate, c);
     }
-    const float r_y = p.rstd[2 * m], r_z = p.rstd[2 * m + 1];
+  };
+  auto weights = [&](int v) {
+    const int c = col(v);
+    wp[v] = wn[v] = wg[v] = zero;
+    if (c >= H) return;
+    if (has_post) wp[v] = ld(p.w_post, c);
+    if (has_dh) wn[v] = ld(p.w_next, c);
+    if constexpr (GATE == GATE_ROW) wg[v] = ld(p.gate, c);
+  };
+  if constexpr (AHEAD)
+#pragma unroll
+    for (int v = 0; v < V; ++v) weights(v);
+  NormRow<V, GATE> cur, next;
+  const int64_t step = (int64_t)gridDim.x * slots;
+  // a slot past the last row repeats it and keeps nothing (its waves still meet the others at the barrier)
+  int64_t m = (int64_t)blockIdx.x * slots + slot;
+  load(m < p.M ? m : p.M - 1, cur);
+  int turn = 0;
+  for (int64_t base = (int64_t)blockIdx.x * slots; base < p.M; base += step, m += step, turn ^= 1) {
+    const bool live = m < p.M;
+    if constexpr (AHEAD) load(m + step < p.M ? m + step : p.M - 1, next);
+    const float r_y = cur.r_y, r_z = cur.r_z;
     float g0[V][8], s[3] = {0.0f, 0.0f, 0.0f};  // g0 = dz + r_z dn
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int c = (threadIdx.x + v * blockDim.x) * 8;
-      float z[8], q[8], f[8];
-      row_widen<T>(gv[v], g0[v]);
-      row_widen<T>(zv[v], z);
-      if (p.dh && c < H) {
+      if constexpr (!AHEAD) weights(v);
+      float z[8], f[8];
+      row_widen<T>(cur.dz[v], g0[v]);
+      row_widen<T>(cur.z[v], z);
+      if (has_dh) {
         float dh[8];
-        row_widen<T>(dv[v], dh);
-        row_widen<T>(row_ld(p.w_next, c, H), f);
+        row_widen<T>(cur.dh[v], dh);
+        row_widen<T>(wn[v], f);
+        const float k = live ? r_z : 0.0f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          an[v][e] = fmaf(dh[e], z[e] * r_z, an[v][e]);
+          an[v][e] = fmaf(dh[e], z[e] * k, an[v][e]);
           const float dn = dh[e] * f[e];
           s[0] = fmaf(dn, z[e], s[0]);
           g0[v][e] = fmaf(r_z, dn, g0[v][e]);
         }
       }
-      if (p.w_post && c < H) {
-        row_widen<T>(yv[v], q);
-        row_widen<T>(row_ld(p.w_post, c, H), f);
+      if (has_post) {
+        float q[8];
+        row_widen<T>(cur.y[v], q);
+        row_widen<T>(wp[v], f);
 #pragma unroll
         for (int e = 0; e < 8; ++e) q[e] *= f[e];
-        if (p.gate) {
-          row_widen<T>(row_ld(p.gate + m * p.ld_gate, c, H), f);
+        if constexpr (GATE != GATE_NONE) {
+          row_widen<T>(GATE == GATE_FULL ? cur.gate[v] : wg[v], f);
 #pragma unroll
           for (int e = 0; e < 8; ++e) q[e] *= f[e];
         }
@@ -181,124 +254,189 @@ __global__ __launch_bounds__(1024) void k_norm_bwd(NormBwdParams p) {
         }
       }
     }
-    row_sums(s, red[turn][0]);  // two sets in turn: no barrier between a row's reads and the next row's writes
-    const float cz = p.dh ? r_z * r_z * r_z * (s[0] * inv_h) : 0.0f;
-    const float cy = p.w_post ? r_y * r_y * r_y * ((s[1] - cz * s[2]) * inv_h) : 0.0f;
+    row_sums(s, red[turn], w0, waves);  // two sets in turn: no barrier between a row's reads and the next row's writes
+    const float cz = has_dh ? r_z * r_z * r_z * (s[0] * inv_h) : 0.0f;
+    const float cy = has_post ? r_y * r_y * r_y * ((s[1] - cz * s[2]) * inv_h) : 0.0f;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int c = (threadIdx.x + v * blockDim.x) * 8;
-      if (c >= H) continue;
+      const int c = col(v);
+      if (c >= H || !live) continue;
+      if constexpr (!AHEAD) weights(v);
       float z[8], o[8];
-      row_widen<T>(zv[v], z);
+      row_widen<T>(cur.z[v], z);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         g0[v][e] = fmaf(-cz, z[e], g0[v][e]);
         o[e] = p.alpha * g0[v][e];
       }
-      row_st(p.dres + m * p.ld_dres, c, H, row_narrow<T>(o));
-      if (!p.y) continue;
+      st(p.dres + m * p.ld_dres, c, row_narrow<T>(o));
+      if (!has_y) continue;
       float y[8], w[8], f[8];
-      row_widen<T>(yv[v], y);
+      row_widen<T>(cur.y[v], y);
 #pragma unroll
       for (int e = 0; e < 8; ++e) w[e] = 1.0f;
-      if (p.w_post) row_widen<T>(row_ld(p.w_post, c, H), w);
-      if (p.gate) {  // dgate = G t, t = y r_y w_post
+      if (has_post) row_widen<T>(wp[v], w);
+      if constexpr (GATE != GATE_NONE) {  // dgate = G t, t = y r_y w_post
 #pragma unroll
         for (int e = 0; e < 8; ++e) o[e] = g0[v][e] * (y[e] * r_y * w[e]);
-        if (p.ld_gate == 0) {
+        if constexpr (GATE == GATE_ROW) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) ag[v][e] += o[e];
         } else if (p.dgate) {
-          row_st(p.dgate + m * p.ld_dgate, c, H, row_narrow<T>(o));
+          st(p.dgate + m * p.ld_dgate, c, row_narrow<T>(o));
         }
-        row_widen<T>(row_ld(p.gate + m * p.ld_gate, c, H), f);
+        row_widen<T>(GATE == GATE_FULL ? cur.gate[v] : wg[v], f);
 #pragma unroll
         for (int e = 0; e < 8; ++e) g0[v][e] *= f[e];
       }
-      if (p.w_post) {
+      if (has_post) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           ap[v][e] = fmaf(g0[v][e], y[e] * r_y, ap[v][e]);
           g0[v][e] = fmaf(r_y * w[e], g0[v][e], -cy * y[e]);
         }
       }
-      row_st(p.dy + m * p.ld_dy, c, H, row_narrow<T>(g0[v]));
+      st(p.dy + m * p.ld_dy, c, row_narrow<T>(g0[v]));
     }
+    if constexpr (AHEAD) cur = next;
+    else load(m + step < p.M ? m + step : p.M - 1, cur);
   }
   const int64_t ldp = (p.H + 7) & ~(int64_t)7;
-  float *out = p.part + (int64_t)blockIdx.x * ldp;
-  const int64_t stride = (int64_t)gridDim.x * ldp;
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const int c = (threadIdx.x + v * blockDim.x) * 8;
-    if (c >= H) continue;
+  for (int k = 0; k < 3; ++k) {
+    if (k == 0 ? !p.dw_post : k == 1 ? !p.dw_next : GATE != GATE_ROW || !p.dgate) continue;
+    auto &sum = k == 0 ? ap : k == 1 ? an : ag;
+    // the row slots one after the other; the last writes the workgroup's part
+    for (int t = 0; t < slots; ++t) {
+      if (slots > 1) __syncthreads();
+      if (slot != t) continue;
+      float *out = t == slots - 1 ? p.part + ((int64_t)k * gridDim.x + blockIdx.x) * ldp : cols;
 #pragma unroll
-    for (int e = 0; e < 8; e += 4) {
-      if (p.dw_post) *reinterpret_cast<f32x4 *>(out + c + e) = f32x4{ap[v][e], ap[v][e + 1], ap[v][e + 2], ap[v][e + 3]};
-      if (p.dw_next) *reinterpret_cast<f32x4 *>(out + stride + c + e) = f32x4{an[v][e], an[v][e + 1], an[v][e + 2], an[v][e + 3]};
-      if (p.dgate && p.ld_gate == 0)
-        *reinterpret_cast<f32x4 *>(out + 2 * stride + c + e) = f32x4{ag[v][e], ag[v][e + 1], ag[v][e + 2], ag[v][e + 3]};
+      for (int v = 0; v < V; ++v) {
+        const int c = col(v);
+        if (c >= H) continue;
+#pragma unroll
+        for (int e = 0; e < 8; e += 4) {
+          f32x4 a = {sum[v][e], sum[v][e + 1], sum[v][e + 2], sum[v][e + 3]};
+          if (t > 0) a = *reinterpret_cast<const f32x4 *>(cols + c + e) + a;
+          *reinterpret_cast<f32x4 *>(out + c + e) = a;
+        }
+      }
     }
+    if (slots > 1) __syncthreads();
   }
 }
 
-// Column sums over the workgroups' parts: 64 columns per workgroup, 4 waves
-// each over a contiguous quarter of the parts, the quarters added in order.
+// Column sums over the workgroups' parts: 64 columns per workgroup, 16 waves
+// each over a contiguous sixteenth of the parts, the sixteenths added in order.
+constexpr int kSumWaves = 16;
+
 template <class T>
-__global__ __launch_bounds__(256) void k_norm_wgrad(NormBwdParams p) {
-  __shared__ float red[4][64];
+__global__ __launch_bounds__(64 * kSumWaves) void k_norm_wgrad(NormBwdParams p) {
+  __shared__ float red[kSumWaves][64];
   const int which = blockIdx.y, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   uint16_t *out = which == 0 ? p.dw_post : which == 1 ? p.dw_next : p.ld_gate == 0 ? p.dgate : nullptr;
   if (!out) return;
   const int64_t ldp = (p.H + 7) & ~(int64_t)7, c = (int64_t)blockIdx.x * 64 + lane;
-  const int lo = p.groups * wave / 4, hi = p.groups * (wave + 1) / 4;
+  const int lo = p.groups * wave / kSumWaves, hi = p.groups * (wave + 1) / kSumWaves;
+  const float *part = p.part + (int64_t)which * p.groups * ldp + c;
   float t = 0.0f;
-  if (c < p.H)
-    for (int g = lo; g < hi; ++g) t += p.part[((int64_t)which * p.groups + g) * ldp + c];
+  if (c < p.H) {
+#pragma unroll 8
+    for (int g = lo; g < hi; ++g) t += part[g * ldp];
+  }
   red[wave][lane] = t;
   __syncthreads();
-  if (wave == 0 && c < p.H) out[c] = T::r(((red[0][lane] + red[1][lane]) + red[2][lane]) + red[3][lane]);
+  if (wave == 0 && c < p.H) {
+#pragma unroll
+    for (int w = 1; w < kSumWaves; ++w) t += red[w][lane];
+    out[c] = T::r(t);
+  }
 }
 
-// Threads of a row: 8 elements each while 1024 threads hold the row, else 16.
-int row_threads(int64_t H) {
-  const int64_t chunks = (H + 7) / 8;
-  if (chunks > 1024) return 1024;
-  return (int)((chunks + 63) / 64 * 64);
+// Threads of a row that take V chunks of 8 each, in whole waves.
+int row_threads(int64_t H, int V) {
+  const int64_t chunks = (H + 7) / 8, threads = (chunks + V - 1) / V;
+  return (int)((threads + 63) / 64 * 64);
+}
+
+// Chunks of 8 a backward thread: with two, half the reductions and no spilled
+// registers (4096 x 4096: 37 us against 48, 16384 x 1024: 41 against 45); below
+// 1024 a wave would be left half empty (3000 x 700: 29 us against 26).
+int bwd_chunks(int64_t H) { return H < 1024 ? 1 : H <= 16 * kBwdThreads ? 2 : 4; }
+
+// Workgroups that fit the card at once: two a CU with V = 1, else one.
+int64_t bwd_most_groups(int64_t H) { return bwd_chunks(H) == 1 ? 512 : 256; }
+
+// Rows a workgroup holds at a time: as many as its threads take, but no more
+// than keep all CUs at work.
+int bwd_slots(int64_t M, int64_t H) {
+  const int64_t fit = kBwdThreads / row_threads(H, bwd_chunks(H)), want = (M + bwd_most_groups(H) - 1) / bwd_most_groups(H);
+  return (int)(want < fit ? want : fit);
 }
 
 }  // namespace
 
 hipError_t launch_norm_fwd(const NormFwdParams &p, hipStream_t s) {
-  const dim3 g((unsigned)p.M), b(row_threads(p.H));
-  if (p.H <= 8192) {
-    if (p.fmt == FMT_F16) dgf_launch((k_norm_fwd<F16, 1>), g, b, 0, s, p);
-    else dgf_launch((k_norm_fwd<Bf16, 1>), g, b, 0, s, p);
-  } else {
-    if (p.fmt == FMT_F16) dgf_launch((k_norm_fwd<F16, 2>), g, b, 0, s, p);
-    else dgf_launch((k_norm_fwd<Bf16, 2>), g, b, 0, s, p);
+  const int V = p.H <= 8192 ? 1 : 2;
+  const dim3 g((unsigned)p.M), b(row_threads(p.H, V));
+#define DGF_NORM_FWD(T, V_, WHOLE) dgf_launch((k_norm_fwd<T, V_, WHOLE>), g, b, 0, s, p)
+  switch (4 * (p.fmt == FMT_F16) + 2 * (V == 2) + (p.H % 8 == 0)) {
+    case 0: DGF_NORM_FWD(Bf16, 1, false); break;
+    case 1: DGF_NORM_FWD(Bf16, 1, true); break;
+    case 2: DGF_NORM_FWD(Bf16, 2, false); break;
+    case 3: DGF_NORM_FWD(Bf16, 2, true); break;
+    case 4: DGF_NORM_FWD(F16, 1, false); break;
+    case 5: DGF_NORM_FWD(F16, 1, true); break;
+    case 6: DGF_NORM_FWD(F16, 2, false); break;
+    default: DGF_NORM_FWD(F16, 2, true); break;
   }
+#undef DGF_NORM_FWD
   return hipGetLastError();
 }
 
-int norm_bwd_groups(int64_t M, int64_t H) { return (int)(M < 512 ? M : 512); }
+int norm_bwd_groups(int64_t M, int64_t H) {
+  const int64_t most = bwd_most_groups(H), slots = bwd_slots(M, H), need = (M + slots - 1) / slots;
+  return (int)(need < most ? need : most);
+}
+
+template <class T, int V, int GATE>
+static void norm_bwd_v(const NormBwdParams &p, hipStream_t s) {
+  const int rt = row_threads(p.H, V), slots = bwd_slots(p.M, p.H);
+  const dim3 g((unsigned)p.groups), b(rt * slots);
+  const size_t lds = slots > 1 ? (size_t)((p.H + 7) & ~(int64_t)7) * 4 : 0;
+  const bool all = V <= 2 && p.dz && p.dh && p.y && p.w_post;
+  if (!all) dgf_launch((k_norm_bwd<T, V, GATE, false, false>), g, b, lds, s, p, rt);
+  else if (p.H % 8 == 0) dgf_launch((k_norm_bwd<T, V, GATE, true, true>), g, b, lds, s, p, rt);
+  else dgf_launch((k_norm_bwd<T, V, GATE, true, false>), g, b, lds, s, p, rt);
+}
+
+template <class T, int GATE>
+static void norm_bwd_t(const NormBwdParams &p, hipStream_t s) {
+  switch (bwd_chunks(p.H)) {
+    case 1: norm_bwd_v<T, 1, GATE>(p, s); break;
+    case 2: norm_bwd_v<T, 2, GATE>(p, s); break;
+    default: norm_bwd_v<T, 4, GATE>(p, s); break;
+  }
+}
 
 hipError_t launch_norm_bwd(const NormBwdParams &p, hipStream_t s) {
-  const dim3 g((unsigned)p.groups), b(row_threads(p.H));
-  if (p.H <= 8192) {
-    if (p.fmt == FMT_F16) dgf_launch((k_norm_bwd<F16, 1>), g, b, 0, s, p);
-    else dgf_launch((k_norm_bwd<Bf16, 1>), g, b, 0, s, p);
-  } else {
-    if (p.fmt == FMT_F16) dgf_launch((k_norm_bwd<F16, 2>), g, b, 0, s, p);
-    else dgf_launch((k_norm_bwd<Bf16, 2>), g, b, 0, s, p);
+  const int gate = !p.gate ? GATE_NONE : p.ld_gate == 0 ? GATE_ROW : GATE_FULL;
+  switch (gate * 2 + (p.fmt == FMT_F16)) {
+    case 0: norm_bwd_t<Bf16, GATE_NONE>(p, s); break;
+    case 1: norm_bwd_t<F16, GATE_NONE>(p, s); break;
+    case 2: norm_bwd_t<Bf16, GATE_ROW>(p, s); break;
+    case 3: norm_bwd_t<F16, GATE_ROW>(p, s); break;
+    case 4: norm_bwd_t<Bf16, GATE_FULL>(p, s); break;
+    default: norm_bwd_t<F16, GATE_FULL>(p, s); break;
   }
   return hipGetLastError();
 }
 
 hipError_t launch_norm_wgrad(const NormBwdParams &p, hipStream_t s) {
   const dim3 g((unsigned)((p.H + 63) / 64), 3);
-  if (p.fmt == FMT_F16) dgf_launch(k_norm_wgrad<F16>, g, dim3(256), 0, s, p);
-  else dgf_launch(k_norm_wgrad<Bf16>, g, dim3(256), 0, s, p);
+  if (p.fmt == FMT_F16) dgf_launch(k_norm_wgrad<F16>, g, dim3(64 * kSumWaves), 0, s, p);
+  else dgf_launch(k_norm_wgrad<Bf16>, g, dim3(64 * kSumWaves), 0, s, p);
   return hipGetLastError();
 }
 

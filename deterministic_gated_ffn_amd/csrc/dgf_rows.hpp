@@ -31,4 +31,19 @@ __device__ __forceinline__ uint4 row_narrow(const float (&f)[8]) {
                     T::pack_prod(f[6], f[7]));
 }
 
+// The sum of v over the wave, in lane 63 (only): shifts within rows of 16
+// lanes, then row ends broadcast (data-parallel moves, no trip through LDS).
+__device__ __forceinline__ float wave_sum_last(float v) {
+#define DGF_SUM_STEP(ctrl, rows) \
+  v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), ctrl, rows, 0xf, false));
+  DGF_SUM_STEP(0x111, 0xf)  // row_shr:1
+  DGF_SUM_STEP(0x112, 0xf)  // row_shr:2
+  DGF_SUM_STEP(0x114, 0xf)  // row_shr:4
+  DGF_SUM_STEP(0x118, 0xf)  // row_shr:8
+  DGF_SUM_STEP(0x142, 0xa)  // row_bcast:15
+  DGF_SUM_STEP(0x143, 0xc)  // row_bcast:31
+#undef DGF_SUM_STEP
+  return v;
+}
+
 }  // namespace dgf
