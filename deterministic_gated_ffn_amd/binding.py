@@ -111,11 +111,14 @@ def _stream(stream=None) -> int:
     return stream.cuda_stream
 
 
+_ON_CURRENT = contextlib.nullcontext()
+
+
 def _on(stream):
     """Allocate on the launch stream: outputs and the workspace come from that
     stream's pool, so the caching allocator cannot hand a block to another
     stream while the launched kernels still use it."""
-    return torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext()
+    return torch.cuda.stream(stream) if stream is not None else _ON_CURRENT
 
 
 DGF_BF16, DGF_FP16, DGF_FP32 = 0, 1, 2
@@ -153,7 +156,7 @@ def _empty(rows: int, cols: int, like: torch.Tensor, ld: int | None = None) -> t
 
 
 def _workspace(nbytes: int, like: torch.Tensor) -> torch.Tensor:
-    return torch.empty(max(int(nbytes), 16), dtype=torch.uint8, device=like.device)
+    return like.new_empty(max(int(nbytes), 16), dtype=torch.uint8)
 
 
 # ---------------------------------------------------------------- entry points
@@ -380,7 +383,7 @@ def _rows(t, shape, like: torch.Tensor, name: str):
         return None, 0
     if t.dtype != like.dtype or t.device != like.device:
         raise TypeError(f"{name}: expected {like.dtype} on {like.device}, got {t.dtype} on {t.device}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     return _mat(t, name)
 
@@ -406,6 +409,8 @@ def norm_fwd(res, y=None, w_post=None, gate=None, alpha: float = 1.0, w_next=Non
     L = load()
     dt = _stored(res)
     M, H = res.shape
+    if y is None and out is not None:
+        raise ValueError("out: without y there is no new residual (z is res)")
     rp, ldr = _mat(res, "res")
     yp, ldy = _rows(y, (M, H), res, "y")
     gp, ldg = _gate(gate, M, H, res)
@@ -413,8 +418,8 @@ def norm_fwd(res, y=None, w_post=None, gate=None, alpha: float = 1.0, w_next=Non
     with _on(stream):
         z = res if y is None else _empty(M, H, res) if out is None else out
         h = _empty(M, H, res) if w_next is not None else None
-        rstd = torch.empty((M, 2), dtype=torch.float32, device=res.device) if training else None
-    zp, ldz = _rows(z, (M, H), res, "out")
+        rstd = res.new_empty((M, 2), dtype=torch.float32) if training else None
+    zp, ldz = _rows(z, (M, H), res, "out") if out is not None else (z.data_ptr(), z.stride(0))
     hp, ldh = (h.data_ptr(), h.stride(0)) if h is not None else (None, 0)
     _check(L.dgf_norm_fwd(rp, ldr, yp, ldy, wp, gp, ldg, alpha, wn, eps, zp, ldz, hp, ldh,
                           rstd.data_ptr() if training else None, M, H, dt, _stream(stream)), "dgf_norm_fwd")
@@ -478,8 +483,9 @@ class Packed8(NamedTuple):
 
 def _packed(M: int, N: int, like: torch.Tensor) -> Packed8:
     ld = (N + 15) // 16 * 16
-    codes = torch.empty((M, ld), dtype=torch.int8, device=like.device)[:, :N]
-    return Packed8(codes, torch.empty((M, -(-N // BLOCK8)), dtype=torch.float32, device=like.device), like.dtype)
+    codes = like.new_empty((M, ld), dtype=torch.int8)
+    scales = like.new_empty((M, -(-N // BLOCK8)), dtype=torch.float32)
+    return Packed8(codes if ld == N else codes[:, :N], scales, like.dtype)
 
 
 def _q8(p: Packed8, shape, dtype, device, name: str):
@@ -488,7 +494,9 @@ def _q8(p: Packed8, shape, dtype, device, name: str):
     M, N = shape
     if p.dtype != dtype or q.dtype != torch.int8 or s.dtype != torch.float32 or q.device != device or s.device != device:
         raise TypeError(f"{name}: expected an 8-bit checkpoint of {dtype} on {device} (int8 codes, float32 scales)")
-    if tuple(q.shape) != (M, N) or tuple(s.shape) != (M, -(-N // BLOCK8)):
+    if not q.is_cuda:
+        raise ValueError(f"{name}: expected GPU tensors")
+    if q.shape != (M, N) or s.shape != (M, -(-N // BLOCK8)):
         raise ValueError(f"{name}: codes {tuple(q.shape)} and scales {tuple(s.shape)} are not those of a {M} x {N} matrix")
     if (N > 1 and q.stride(1) != 1) or (s.shape[1] > 1 and s.stride(1) != 1):
         raise ValueError(f"{name}: expected row-major codes and scales")
@@ -516,7 +524,8 @@ def unpack8(p: Packed8, stream=None) -> torch.Tensor:
     M, N = p.codes.shape
     qp, ldq, sp, lds = _q8(p, (M, N), p.dtype, p.codes.device, "p")
     with _on(stream):
-        t = torch.empty((M, (N + 7) // 8 * 8), dtype=p.dtype, device=p.codes.device)[:, :N]
+        t = p.codes.new_empty((M, (N + 7) // 8 * 8), dtype=p.dtype)
+        t = t if t.shape[1] == N else t[:, :N]
     _check(L.dgf_unpack8(qp, ldq, sp, lds, t.data_ptr(), t.stride(0), M, N, _STORED[p.dtype], _stream(stream)),
            "dgf_unpack8")
     return t
@@ -585,7 +594,7 @@ def _experts(t: torch.Tensor, shape, like: torch.Tensor, name: str):
     """(pointer, leading dimension, expert stride) of the experts' matrices [El, rows, cols]."""
     if t.dtype != like.dtype or t.device != like.device:
         raise TypeError(f"{name}: expected {like.dtype} on {like.device}, got {t.dtype} on {t.device}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.stride(2) != 1:
         raise ValueError(f"{name}: expected row-major matrices (stride(2) == 1)")
@@ -603,7 +612,7 @@ def moe_fwd(x, w_router, w_gate, w_up, w_down, top_k: int, renorm: bool = True, 
     L = load()
     dt = _stored(x)
     M, H = x.shape
-    E, (El, I) = w_router.shape[0], w_gate.shape[:2]
+    E, El, I = w_router.shape[0], w_gate.shape[0], w_gate.shape[1]
     xp, ldx = _mat(x, "x")
     wr, ldr = _rows(w_router, (E, H), x, "w_router")
     wg, ldg, sg = _experts(w_gate, (El, I, H), x, "w_gate")

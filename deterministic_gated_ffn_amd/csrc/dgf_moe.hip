@@ -24,18 +24,12 @@
 #include <math.h>
 
 #include "dgf_block.hpp"
-#include "dgf_device.hpp"
+#include "dgf_rows.hpp"
 
 namespace dgf {
 namespace {
 
 constexpr int kWaves = 8;  // of the gate/up and down workgroups
-
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
-  return v;
-}
 
 // Router products, on the vector unit in FP32 (the matrix core truncates, and
 // a logit's last bits decide ties): a workgroup per expert and kLogitTokens
@@ -65,8 +59,8 @@ __global__ __launch_bounds__(256) void k_moe_logits(MoeParams p) {
   }
 #pragma unroll
   for (int t = 0; t < kLogitTokens; ++t) {
-    const float l = wave_sum(acc[t]);
-    if (lane == 0) red[wave][t] = l;
+    const float l = wave_sum_last(acc[t]);
+    if (lane == 63) red[wave][t] = l;
   }
   __syncthreads();
   const int t = threadIdx.x;
@@ -98,25 +92,22 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
   return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
 }
 
-// One workgroup: a wave per token chooses its experts (NL logits a lane, E <=
-// 64 NL), then a thread per expert lists its tokens.
-constexpr int kRouteThreads = 1024;
-
+// A wave chooses the experts of tokens first, first + step, ... (NL logits a
+// lane, E <= 64 NL); ids: a copy in LDS, or null.
 template <int NL>
-__global__ __launch_bounds__(kRouteThreads) void k_moe_route(MoeParams p) {
-  __shared__ __attribute__((aligned(16))) int ids[kMoeMaxM * kMoeMaxK];
-  __shared__ int sums[kRouteThreads / 64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = kRouteThreads / 64;
-  const int n = p.M * p.k;
-  for (int m = wave; m < p.M; m += waves) {
-    const float *l = p.logits + m * p.E;
+__device__ __forceinline__ void choose(const MoeParams &p, int first, int step, int lane, int *ids) {
+  float next[NL];
+  auto fetch = [&](int m) {
+#pragma unroll
+    for (int i = 0; i < NL; ++i) next[i] = m < p.M && lane + 64 * i < p.E ? p.logits[m * p.E + lane + 64 * i] : -INFINITY;
+  };
+  fetch(first);
+  for (int m = first; m < p.M; m += step) {
     float v[NL];
     uint32_t key[NL];
 #pragma unroll
-    for (int i = 0; i < NL; ++i) {
-      const int e = lane + 64 * i;
-      v[i] = e < p.E ? l[e] : -INFINITY;
-    }
+    for (int i = 0; i < NL; ++i) v[i] = next[i];
+    fetch(m + step);  // the next token's logits arrive during this one's choice
 #pragma unroll
     for (int i = 0; i < NL; ++i) key[i] = lane + 64 * i < p.E ? logit_key(v[i]) : 0u;
     float mine = -INFINITY, top = 0.0f;  // top: the first chosen, the largest
@@ -153,27 +144,62 @@ __global__ __launch_bounds__(kRouteThreads) void k_moe_route(MoeParams p) {
       for (int i = 0; i < NL; ++i)
         if (lane + 64 * i < p.E) part += expf(v[i] - top);
     }
-    const float sum = wave_sum(part);
+    const float sum = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(wave_sum_last(part)), 63));
     if (lane < p.k) {
       const float w = expf(mine - top) / sum;
       const int at = m * p.k + lane;
-      ids[at] = chosen;
+      if (ids) ids[at] = chosen;
       p.ids[at] = chosen;
       p.p[at] = w;
       if (p.ids_out) p.ids_out[at] = chosen;
       if (p.p_out) p.p_out[at] = w;
     }
   }
-  if (threadIdx.x < 4 && n + (int)threadIdx.x < kMoeMaxM * kMoeMaxK) ids[n + threadIdx.x] = -1;
+}
+
+// One workgroup orders all pairs by expert from ids in LDS: a thread per pair,
+// one per expert.
+constexpr int kRouteThreads = 1024;
+static_assert(kRouteThreads >= kMoeMaxE && kMoeMaxE == 1 << 10, "a thread per expert, 10 bits of index");
+
+__device__ __forceinline__ void order(const MoeParams &p, const int *ids, int *cnt, int *sums) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n = p.M * p.k;
+  constexpr int waves = kRouteThreads / 64;
+  cnt[threadIdx.x] = 0;
   __syncthreads();
-  // thread e: local expert e's tokens; (slots << 16 | pairs) before it by a scan
-  const int want = (int)threadIdx.x < p.El ? p.e0 + (int)threadIdx.x : -2;
-  int cnt = 0;
-  for (int b = 0; b < n; b += 4) {
-    const int4 q = *reinterpret_cast<const int4 *>(&ids[b]);
-    cnt += (q.x == want) + (q.y == want) + (q.z == want) + (q.w == want);
+  // thread i: how many pairs before pair i (and i + 1024) have its expert.
+  // Within a wave by matching the index bit by bit, then the waves in turn
+  // (ascending pairs) through each expert's running count.
+  constexpr int PER = kMoeMaxM * kMoeMaxK / kRouteThreads;
+  int mine[PER], rank[PER];
+#pragma unroll
+  for (int u = 0; u < PER; ++u) {
+    const int i = threadIdx.x + u * kRouteThreads;
+    mine[u] = i < n ? ids[i] - p.e0 : -1;
+    if (mine[u] >= p.El) mine[u] = -1;
+    uint64_t same = __ballot(mine[u] >= 0);
+#pragma unroll
+    for (int b = 0; b < 10; ++b) {
+      const uint64_t set = __ballot(mine[u] >> b & 1);
+      same &= mine[u] >> b & 1 ? set : ~set;
+    }
+    const int lead = mine[u] >= 0 ? __ffsll((unsigned long long)same) - 1 : lane;
+    for (int w = 0; w < waves && u * kRouteThreads + w * 64 < n; ++w) {
+      if (wave == w) {
+        int base = 0;
+        if (mine[u] >= 0 && lane == lead) {
+          base = cnt[mine[u]];
+          cnt[mine[u]] = base + __popcll(same);
+        }
+        rank[u] = __shfl(base, lead) + __popcll(same & ((1ull << lane) - 1));
+      }
+      __syncthreads();
+    }
   }
-  int scan = cnt | (cnt > 0) << 16;
+  // thread e: local expert e's slot and first pair, (slots << 16 | pairs) before it by a scan
+  const int have = (int)threadIdx.x < p.El ? cnt[threadIdx.x] : 0;
+  const int own = have | (have > 0) << 16;
+  int scan = own;
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) {
     const int b = __shfl_up(scan, o);
@@ -187,18 +213,42 @@ __global__ __launch_bounds__(kRouteThreads) void k_moe_route(MoeParams p) {
     before += w < wave ? sums[w] : 0;
     total += sums[w];
   }
-  before += scan - (cnt | (cnt > 0) << 16);
+  before += scan - own;
   if (threadIdx.x == 0) p.slots[0] = total >> 16;
-  if (cnt > 0) {
-    const int start = before & 0xffff;
+  if (have > 0) {
     int *slot = p.slots + 1 + 3 * (before >> 16);
     slot[0] = threadIdx.x;
-    slot[1] = start;
-    slot[2] = cnt;
-    int c = 0;
-    for (int i = 0; i < n && c < cnt; ++i)
-      if (ids[i] == want) p.pairs[start + c++] = i;
+    slot[1] = before & 0xffff;
+    slot[2] = have;
   }
+  cnt[threadIdx.x] = before & 0xffff;  // each thread its own entry, read above
+  __syncthreads();
+#pragma unroll
+  for (int u = 0; u < PER; ++u)
+    if (mine[u] >= 0) p.pairs[cnt[mine[u]] + rank[u]] = threadIdx.x + u * kRouteThreads;
+}
+
+template <int NL>
+__global__ __launch_bounds__(kRouteThreads) void k_moe_route(MoeParams p) {
+  __shared__ __attribute__((aligned(16))) int ids[kMoeMaxM * kMoeMaxK];
+  __shared__ int cnt[kMoeMaxE], sums[kRouteThreads / 64];
+  choose<NL>(p, threadIdx.x >> 6, kRouteThreads / 64, threadIdx.x & 63, ids);
+  order(p, ids, cnt, sums);
+}
+
+// The same in two launches for more tokens, whose choices keep one CU busy for
+// longer than a launch takes.
+template <int NL>
+__global__ __launch_bounds__(256) void k_moe_choose(MoeParams p) {
+  const int m = blockIdx.x * 4 + (threadIdx.x >> 6);
+  choose<NL>(p, m, p.M, threadIdx.x & 63, nullptr);
+}
+
+__global__ __launch_bounds__(kRouteThreads) void k_moe_order(MoeParams p) {
+  __shared__ __attribute__((aligned(16))) int ids[kMoeMaxM * kMoeMaxK];
+  __shared__ int cnt[kMoeMaxE], sums[kRouteThreads / 64];
+  for (int i = threadIdx.x; i < p.M * p.k; i += kRouteThreads) ids[i] = p.ids[i];
+  order(p, ids, cnt, sums);
 }
 
 // The two diagonal 8 x 8 blocks of an accumulator added: rows 4 q + i (q < 2)
@@ -544,12 +594,18 @@ __global__ __launch_bounds__(256) void k_moe_combine(MoeParams p) {
   const int h = blockIdx.x * 256 + threadIdx.x, m = blockIdx.y;
   if (h >= p.H) return;
   float y = 0.0f;
-#pragma unroll 4
-  for (int j = 0; j < p.k; ++j) {
-    const int e = p.ids[m * p.k + j] - p.e0;
-    const bool local = e >= 0 && e < p.El;  // prod holds nothing for the others
-    const float t = local ? p.prod[(int64_t)(m * p.k + j) * p.H + h] : 0.0f;
-    y = local ? fmaf(p.p[m * p.k + j], t, y) : y;
+  for (int j0 = 0; j0 < p.k; j0 += 8) {
+    float t[8], w[8];
+    bool here[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {  // all loads first; prod holds nothing for experts of other calls
+      const int at = m * p.k + (j0 + j < p.k ? j0 + j : p.k - 1), e = p.ids[at] - p.e0;
+      t[j] = p.prod[(int64_t)at * p.H + h];
+      w[j] = p.p[at];
+      here[j] = j0 + j < p.k && e >= 0 && e < p.El;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) y = here[j] ? fmaf(w[j], t[j], y) : y;
   }
   p.y[m * p.ldy + h] = T::r(y);
 }
@@ -656,6 +712,10 @@ void moe_plan(MoeParams &p) {
   }
 }
 
+// Tokens that one workgroup both chooses for and orders (8 of 128 experts: 8.3
+// us at 32 tokens, as much as the two launches; 13.2 at 64 against 8.9).
+constexpr int kRouteOnce = 32;
+
 int64_t moe_down_ld(int I, int k) {
   const int step = 64 * waves_per_slot(k);
   return (int64_t)(I + step - 1) / step * step;
@@ -668,10 +728,21 @@ hipError_t launch_moe_logits(const MoeParams &p, hipStream_t s) {
   return hipGetLastError();
 }
 
-hipError_t launch_moe_route(const MoeParams &p, hipStream_t s) {
-  if (p.E <= 128) dgf_launch(k_moe_route<2>, dim3(1), dim3(kRouteThreads), 0, s, p);
-  else dgf_launch(k_moe_route<kMoeMaxE / 64>, dim3(1), dim3(kRouteThreads), 0, s, p);
+template <int NL>
+static hipError_t route_nl(const MoeParams &p, hipStream_t s) {
+  if (p.M <= kRouteOnce) {
+    dgf_launch(k_moe_route<NL>, dim3(1), dim3(kRouteThreads), 0, s, p);
+    return hipGetLastError();
+  }
+  dgf_launch(k_moe_choose<NL>, dim3((p.M + 3) / 4), dim3(256), 0, s, p);
+  dgf_launch(k_moe_order, dim3(1), dim3(kRouteThreads), 0, s, p);
   return hipGetLastError();
+}
+
+hipError_t launch_moe_route(const MoeParams &p, hipStream_t s) {
+  if (p.E <= 128) return route_nl<2>(p, s);
+  if (p.E <= 256) return route_nl<4>(p, s);
+  return route_nl<kMoeMaxE / 64>(p, s);
 }
 
 hipError_t launch_moe_gate_up(const MoeParams &p, hipStream_t s) {

@@ -14,17 +14,23 @@ namespace {
 constexpr int kThreads = 256;
 
 // A row's blocks padded to whole ones, 8 lanes each: `lanes` (a power of two,
-// 8 to 256) of a workgroup's threads share a row and step over it.
+// 8 to 256) of a workgroup's threads share a row, and grid.y workgroups its
+// columns, `span` of them each: a few chunks of 8 a thread where that still
+// makes 2048 workgroups, one where it does not (32 x 12288 written: 5.8 us with
+// whole rows, 3.0 so; 777 x 5461 in the activation's backward: 15.8 and 13.8).
 struct RowMap {
-  int lanes;
-  unsigned grid;
+  int lanes, span;
+  dim3 grid;
 };
 RowMap row_map(int64_t M, int64_t N) {
   const int64_t chunks = (N + kQ8Block - 1) / kQ8Block * 8;
   int lanes = 8;
   while (lanes < kThreads && lanes < chunks) lanes <<= 1;
-  const int rows = kThreads / lanes;
-  return RowMap{lanes, (unsigned)((M + rows - 1) / rows)};
+  const int64_t rows = kThreads / lanes, groups = (M + rows - 1) / rows;
+  int64_t per = (chunks + lanes - 1) / lanes;  // chunks a thread for whole rows
+  while (per > 1 && groups * ((chunks + lanes * per - 1) / (lanes * per)) < 2048) per = (per + 1) / 2;
+  while ((chunks + lanes * per - 1) / (lanes * per) > 65535) per *= 2;  // grid.y
+  return RowMap{lanes, (int)(lanes * per * 8), dim3((unsigned)groups, (unsigned)((chunks + lanes * per - 1) / (lanes * per)))};
 }
 
 // Rows past M keep their lanes in the loop (the lane exchanges need whole
@@ -33,11 +39,12 @@ RowMap row_map(int64_t M, int64_t N) {
   const int64_t m = (int64_t)blockIdx.x * (kThreads / lanes) + threadIdx.x / lanes;         \
   const bool row_ok = m < (M_);                                                             \
   const int64_t padded = ((N_) + kQ8Block - 1) / kQ8Block * kQ8Block;                       \
-  for (int64_t c = (int64_t)(threadIdx.x & (lanes - 1)) * 8; c < padded; c += 8 * lanes)
+  const int64_t first = (int64_t)blockIdx.y * span, last = first + span < padded ? first + span : padded; \
+  for (int64_t c = first + (threadIdx.x & (lanes - 1)) * 8; c < last; c += 8 * lanes)
 
 template <class T>
 __global__ __launch_bounds__(kThreads) void k_pack8(const uint16_t *x, int64_t ldx, Q8Mat o, int64_t M, int64_t N,
-                                                    int lanes) {
+                                                    int lanes, int span) {
   DGF_ROWS(M, N) {
     const bool in = row_ok && c < N;
     float f[8], s;
@@ -52,7 +59,7 @@ __global__ __launch_bounds__(kThreads) void k_pack8(const uint16_t *x, int64_t l
 
 template <class T>
 __global__ __launch_bounds__(kThreads) void k_unpack8(Q8Mat x, uint16_t *o, int64_t ldo, int64_t M, int64_t N,
-                                                      int lanes) {
+                                                      int lanes, int span) {
   DGF_ROWS(M, N) {
     if (!row_ok || c >= N) continue;
     float f[8];
@@ -62,7 +69,7 @@ __global__ __launch_bounds__(kThreads) void k_unpack8(Q8Mat x, uint16_t *o, int6
 }
 
 template <class T>
-__global__ __launch_bounds__(kThreads) void k_act_bwd_q8(ActQ8Params p, int lanes) {
+__global__ __launch_bounds__(kThreads) void k_act_bwd_q8(ActQ8Params p, int lanes, int span) {
   DGF_ROWS(p.M, p.N) {
     if (!row_ok || c >= p.N) continue;
     float da[8], g[8], u[8];
@@ -71,16 +78,22 @@ __global__ __launch_bounds__(kThreads) void k_act_bwd_q8(ActQ8Params p, int lane
     q8_values(q8_ld(p.u.q + m * p.u.ldq, c, p.N), p.u.s[m * p.u.lds + c / kQ8Block], u);
     uint4 dg, du, a;
     q8_dsilu<T>(da, g, u, dg, du, a);
-    row_st(p.dg + m * p.ldo, c, p.N, dg);
-    row_st(p.du + m * p.ldo, c, p.N, du);
-    if (p.a) row_st(p.a + m * p.ldo, c, p.N, a);
+    if (p.M * p.N >= kStreamElements) {  // 4096 x 12288: 98.6 us against 101
+      row_st_nt(p.dg + m * p.ldo, c, p.N, dg);
+      row_st_nt(p.du + m * p.ldo, c, p.N, du);
+      if (p.a) row_st_nt(p.a + m * p.ldo, c, p.N, a);
+    } else {
+      row_st(p.dg + m * p.ldo, c, p.N, dg);
+      row_st(p.du + m * p.ldo, c, p.N, du);
+      if (p.a) row_st(p.a + m * p.ldo, c, p.N, a);
+    }
   }
 }
 
 // The gate/up join with the activation and the checkpoint: a from the rounded
 // roots g and u (the bits of the 16-bit form), their codes in place of g and u.
 template <class T, int S>
-__global__ __launch_bounds__(kThreads) void k_join_act_q8(GemmParams p, Q8Mat g8, Q8Mat u8, int lanes) {
+__global__ __launch_bounds__(kThreads) void k_join_act_q8(GemmParams p, Q8Mat g8, Q8Mat u8, int lanes, int span) {
   DGF_ROWS(p.M, p.N) {
     const bool in = row_ok && c < p.N;
     uint32_t r0[4] = {0, 0, 0, 0}, r1[4] = {0, 0, 0, 0}, a[4];
@@ -117,7 +130,7 @@ __global__ __launch_bounds__(kThreads) void k_join_act_q8(GemmParams p, Q8Mat g8
 
 // The dA join with the activation's backward from the checkpoint.
 template <class T, int S>
-__global__ __launch_bounds__(kThreads) void k_join_dsilu_q8(GemmParams p, Q8Mat g8, Q8Mat u8, int lanes) {
+__global__ __launch_bounds__(kThreads) void k_join_dsilu_q8(GemmParams p, Q8Mat g8, Q8Mat u8, int lanes, int span) {
   DGF_ROWS(p.M, p.N) {
     if (!row_ok || c >= p.N) continue;
     uint32_t r[4];
@@ -147,24 +160,24 @@ __global__ __launch_bounds__(kThreads) void k_join_dsilu_q8(GemmParams p, Q8Mat 
 
 hipError_t launch_pack8(int fmt, const uint16_t *x, int64_t ldx, Q8Mat o, int64_t M, int64_t N, hipStream_t s) {
   const RowMap r = row_map(M, N);
-  DGF_BY_TYPE(fmt, k_pack8, r.grid, x, ldx, o, M, N, r.lanes);
+  DGF_BY_TYPE(fmt, k_pack8, r.grid, x, ldx, o, M, N, r.lanes, r.span);
 }
 
 hipError_t launch_unpack8(int fmt, Q8Mat x, uint16_t *o, int64_t ldo, int64_t M, int64_t N, hipStream_t s) {
   const RowMap r = row_map(M, N);
-  DGF_BY_TYPE(fmt, k_unpack8, r.grid, x, o, ldo, M, N, r.lanes);
+  DGF_BY_TYPE(fmt, k_unpack8, r.grid, x, o, ldo, M, N, r.lanes, r.span);
 }
 
 hipError_t launch_act_bwd_q8(int fmt, const ActQ8Params &p, hipStream_t s) {
   const RowMap r = row_map(p.M, p.N);
-  DGF_BY_TYPE(fmt, k_act_bwd_q8, r.grid, p, r.lanes);
+  DGF_BY_TYPE(fmt, k_act_bwd_q8, r.grid, p, r.lanes, r.span);
 }
 
 // The joins' K pieces, 2^ksplit_depth of them, are a template argument.
 #define DGF_JOIN(kernel, S_)                                                                                      \
   case S_:                                                                                                        \
-    if (p.fmt == FMT_F16) dgf_launch((kernel<F16, S_>), dim3(r.grid), dim3(kThreads), 0, s, p, g, u, r.lanes);    \
-    else dgf_launch((kernel<Bf16, S_>), dim3(r.grid), dim3(kThreads), 0, s, p, g, u, r.lanes);                    \
+    if (p.fmt == FMT_F16) dgf_launch((kernel<F16, S_>), dim3(r.grid), dim3(kThreads), 0, s, p, g, u, r.lanes, r.span);    \
+    else dgf_launch((kernel<Bf16, S_>), dim3(r.grid), dim3(kThreads), 0, s, p, g, u, r.lanes, r.span);                    \
     break;
 #define DGF_JOINS(kernel)                                                                                         \
   const RowMap r = row_map(p.M, p.N);                                                                             \

@@ -60,9 +60,15 @@ __device__ __forceinline__ void q8_values(const uint2 &q, float s, float (&x)[8]
   for (int e = 0; e < 8; ++e) x[e] = (float)(int8_t)((e < 4 ? q.x : q.y) >> (8 * (e & 3))) * s;
 }
 
-// 8 codes of a row from column c (zeros past N), and back.
+typedef uint64_t u64_any __attribute__((aligned(1)));
+
+// 8 codes of a row from column c (zeros past N; ragged ends as in row_ld), and back.
 __device__ __forceinline__ uint2 q8_ld(const uint8_t *row, int64_t c, int64_t N) {
   if (c + 8 <= N) return *reinterpret_cast<const uint2 *>(row + c);
+  if (N >= 8) {
+    const uint64_t v = *reinterpret_cast<const u64_any *>(row + N - 8) >> (int)(c + 8 - N) * 8;
+    return make_uint2((uint32_t)v, (uint32_t)(v >> 32));
+  }
   uint32_t q[2] = {0, 0};
   for (int e = 0; c + e < N; ++e) q[e >> 2] |= (uint32_t)row[c + e] << (8 * (e & 3));
   return make_uint2(q[0], q[1]);
