@@ -151,8 +151,9 @@ def _mat(t: torch.Tensor, name: str):
 def _empty(rows: int, cols: int, like: torch.Tensor, ld: int | None = None) -> torch.Tensor:
     """Row-major [rows, cols] of like's dtype whose leading dimension is a multiple of 8."""
     ld = ld or ((cols + 7) // 8) * 8
-    buf = like.new_empty((rows, ld))
-    return buf if ld == cols else buf[:, :cols]
+    if ld == cols:  # no padding: the cheapest allocation torch has
+        return torch.empty_like(like) if like.shape == (rows, cols) and like.is_contiguous() else like.new_empty((rows, cols))
+    return like.new_empty((rows, ld))[:, :cols]
 
 
 def _workspace(nbytes: int, like: torch.Tensor) -> torch.Tensor:
@@ -392,6 +393,8 @@ def _gate(gate, M: int, H: int, like: torch.Tensor):
     """(pointer, leading dimension): 0 for one value a channel ([H])."""
     if gate is not None and gate.dim() == 1:
         return _vec(gate, H, like, "gate"), 0
+    if gate is not None and gate.dim() == 2 and gate.stride(0) == 0 and M > 0:
+        raise ValueError("gate: give one value a channel as a vector, not as an expanded matrix")
     return _rows(gate, (M, H), like, "gate")
 
 

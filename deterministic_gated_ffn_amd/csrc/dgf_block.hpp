@@ -75,6 +75,8 @@ struct MoeParams {
 void moe_plan(MoeParams &p);
 // Row length of one part of `a`: I rounded up to whole steps of the down kernel.
 int64_t moe_down_ld(int I, int k);
+// Whether the gate/up kernel chooses the experts itself (no route launch).
+bool moe_one(const MoeParams &p);
 hipError_t launch_moe_logits(const MoeParams &p, hipStream_t s);
 hipError_t launch_moe_route(const MoeParams &p, hipStream_t s);
 hipError_t launch_moe_gate_up(const MoeParams &p, hipStream_t s);

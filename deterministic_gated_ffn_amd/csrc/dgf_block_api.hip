@@ -261,7 +261,7 @@ dgf_status dgf_moe_fwd(const void *x, int64_t ldx, const void *w_router, int64_t
   carve_moe(p, ws);
   hipStream_t s = (hipStream_t)stream;
   DGF_TRY(hip_check(timed(s, "moe logits", [&] { return launch_moe_logits(p, s); }), "moe logits"));
-  DGF_TRY(hip_check(timed(s, "moe route", [&] { return launch_moe_route(p, s); }), "moe route"));
+  if (!moe_one(p)) DGF_TRY(hip_check(timed(s, "moe route", [&] { return launch_moe_route(p, s); }), "moe route"));
   DGF_TRY(hip_check(timed(s, "moe gate/up", [&] { return launch_moe_gate_up(p, s); }), "moe gate/up"));
   DGF_TRY(hip_check(timed(s, "moe down", [&] { return launch_moe_down(p, s); }), "moe down"));
   if (p.split > 1) DGF_TRY(hip_check(timed(s, "moe combine", [&] { return launch_moe_combine(p, s); }), "moe combine"));

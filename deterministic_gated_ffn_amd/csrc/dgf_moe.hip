@@ -31,6 +31,12 @@ namespace {
 
 constexpr int kWaves = 8;  // of the gate/up and down workgroups
 
+}  // namespace
+
+bool moe_one(const MoeParams &p) { return p.M == 1 && p.E <= 256 && p.H >= 8; }
+
+namespace {
+
 // Router products, on the vector unit in FP32 (the matrix core truncates, and
 // a logit's last bits decide ties): a workgroup per expert and kLogitTokens
 // tokens, a lane 8 of every 2048 K.
@@ -92,67 +98,82 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
   return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
 }
 
-// A wave chooses the experts of tokens first, first + step, ... (NL logits a
-// lane, E <= 64 NL); ids: a copy in LDS, or null.
+// A wave chooses the experts of one token from its logits v (NL a lane, E <= 64
+// NL): lane j < k gets choice j and its routing weight.
+template <int NL>
+__device__ __forceinline__ void choose_token(const MoeParams &p, const float (&v)[NL], int lane, int &chosen,
+                                             float &weight) {
+  uint32_t key[NL];
+#pragma unroll
+  for (int i = 0; i < NL; ++i) key[i] = lane + 64 * i < p.E ? logit_key(v[i]) : 0u;
+  float mine = -INFINITY, top = 0.0f;  // top: the first chosen, the largest
+  chosen = 0;
+  for (int j = 0; j < p.k; ++j) {
+    uint32_t best = 0;
+#pragma unroll
+    for (int i = 0; i < NL; ++i) best = key[i] > best ? key[i] : best;
+    best = wave_max(best);
+    // the lowest index that has it, and its logit
+    int e = -1;
+    float le = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+      const uint64_t at = __ballot(key[i] == best);
+      if (e < 0 && at) {
+        const int src = __ffsll((unsigned long long)at) - 1;
+        e = 64 * i + src;
+        le = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v[i]), src));
+        if (lane == src) key[i] = 0u;
+      }
+    }
+    if (j == 0) top = le;
+    if (lane == j) {
+      chosen = e;
+      mine = le;
+    }
+  }
+  float part = 0.0f;
+  if (p.renorm) {
+    part = lane < p.k ? expf(mine - top) : 0.0f;
+  } else {
+#pragma unroll
+    for (int i = 0; i < NL; ++i)
+      if (lane + 64 * i < p.E) part += expf(v[i] - top);
+  }
+  const float sum = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(wave_sum_last(part)), 63));
+  weight = expf(mine - top) / sum;
+}
+
+template <int NL>
+__device__ __forceinline__ void fetch_logits(const MoeParams &p, int m, int lane, float (&v)[NL]) {
+#pragma unroll
+  for (int i = 0; i < NL; ++i) v[i] = m < p.M && lane + 64 * i < p.E ? p.logits[m * p.E + lane + 64 * i] : -INFINITY;
+}
+
+// Choice `lane` of token m, where the later kernels and the caller look for it.
+__device__ __forceinline__ void store_choice(const MoeParams &p, int m, int lane, int chosen, float weight) {
+  const int at = m * p.k + lane;
+  p.ids[at] = chosen;
+  p.p[at] = weight;
+  if (p.ids_out) p.ids_out[at] = chosen;
+  if (p.p_out) p.p_out[at] = weight;
+}
+
+// A wave chooses for tokens first, first + step, ...; ids: a copy in LDS, or null.
 template <int NL>
 __device__ __forceinline__ void choose(const MoeParams &p, int first, int step, int lane, int *ids) {
   float next[NL];
-  auto fetch = [&](int m) {
-#pragma unroll
-    for (int i = 0; i < NL; ++i) next[i] = m < p.M && lane + 64 * i < p.E ? p.logits[m * p.E + lane + 64 * i] : -INFINITY;
-  };
-  fetch(first);
+  fetch_logits(p, first, lane, next);
   for (int m = first; m < p.M; m += step) {
-    float v[NL];
-    uint32_t key[NL];
+    float v[NL], weight;
+    int chosen;
 #pragma unroll
     for (int i = 0; i < NL; ++i) v[i] = next[i];
-    fetch(m + step);  // the next token's logits arrive during this one's choice
-#pragma unroll
-    for (int i = 0; i < NL; ++i) key[i] = lane + 64 * i < p.E ? logit_key(v[i]) : 0u;
-    float mine = -INFINITY, top = 0.0f;  // top: the first chosen, the largest
-    int chosen = 0;
-    for (int j = 0; j < p.k; ++j) {
-      uint32_t best = 0;
-#pragma unroll
-      for (int i = 0; i < NL; ++i) best = key[i] > best ? key[i] : best;
-      best = wave_max(best);
-      // the lowest index that has it, and its logit
-      int e = -1;
-      float le = 0.0f;
-#pragma unroll
-      for (int i = 0; i < NL; ++i) {
-        const uint64_t at = __ballot(key[i] == best);
-        if (e < 0 && at) {
-          const int src = __ffsll((unsigned long long)at) - 1;
-          e = 64 * i + src;
-          le = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v[i]), src));
-          if (lane == src) key[i] = 0u;
-        }
-      }
-      if (j == 0) top = le;
-      if (lane == j) {
-        chosen = e;
-        mine = le;
-      }
-    }
-    float part = 0.0f;
-    if (p.renorm) {
-      part = lane < p.k ? expf(mine - top) : 0.0f;
-    } else {
-#pragma unroll
-      for (int i = 0; i < NL; ++i)
-        if (lane + 64 * i < p.E) part += expf(v[i] - top);
-    }
-    const float sum = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(wave_sum_last(part)), 63));
+    fetch_logits(p, m + step, lane, next);  // the next token's logits arrive during this one's choice
+    choose_token<NL>(p, v, lane, chosen, weight);
     if (lane < p.k) {
-      const float w = expf(mine - top) / sum;
-      const int at = m * p.k + lane;
-      if (ids) ids[at] = chosen;
-      p.ids[at] = chosen;
-      p.p[at] = w;
-      if (p.ids_out) p.ids_out[at] = chosen;
-      if (p.p_out) p.p_out[at] = w;
+      if (ids) ids[m * p.k + lane] = chosen;
+      store_choice(p, m, lane, chosen, weight);
     }
   }
 }
@@ -299,6 +320,10 @@ __device__ __forceinline__ typename T::frag load_column(__amdgpu_buffer_rsrc_t r
 // values at the end, for weights read from I - 8 (see k_moe_down).
 constexpr int kChunk = 2;
 
+// Magnitude bits of the stored type's infinity, one above its largest value.
+template <class T>
+constexpr uint16_t kInfBits = T::code == Bf16::code ? 0x7f80 : 0x7c00;
+
 // First row of the tile at i0: a ragged last tile takes the last 8 rows (the
 // first of them a second time).
 __device__ __forceinline__ int tile_row(int i0, int I) { return i0 + 8 <= I || I < 8 ? i0 : I - 8; }
@@ -306,13 +331,48 @@ __device__ __forceinline__ int tile_row(int i0, int I) { return i0 + 8 <= I || I
 // Where column k of a pair's row has its first part (the second: 64 further on).
 __device__ __forceinline__ int a_at(int k) { return (k >> 6) * 128 + (k & 63); }
 
-template <class T, int NT, int share, bool ONCE, bool SMALL>
+//
+// ONE > 0: a single token, whose choice (E <= 64 ONE) every workgroup makes for
+// itself from the logits instead of waiting for a launch of its own; slot j is
+// then the token's j-th local choice, and the first workgroup leaves the lists
+// for the down kernel (8 of 128 experts: 5.1 us of routing and 12.1 of products
+// become 13.4 us).
+template <class T, int NT, int share, bool ONCE, bool SMALL, int ONE>
 __global__ __launch_bounds__(64 * kWaves, NT == 1 ? 6 : 4) void k_moe_gate_up(MoeParams p) {
   __shared__ __attribute__((aligned(16))) float red[kWaves][2][8 * NT][8];
-  const int n = p.slots[0], e = p.slots[1 + 3 * blockIdx.y], start = p.slots[2 + 3 * blockIdx.y],
-            cnt = p.slots[3 + 3 * blockIdx.y];
-  if ((int)blockIdx.y >= n) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  int e, start, cnt, pair = 0;  // pair: the only one, with ONE
+  if constexpr (ONE > 0) {
+    float v[ONE], weight;
+    int chosen;
+    fetch_logits(p, 0, lane, v);
+    choose_token<ONE>(p, v, lane, chosen, weight);
+    const int le = chosen - p.e0;
+    const uint64_t local = __ballot(lane < p.k && le >= 0 && le < p.El);
+    const int n = __popcll(local), slot = __popcll(local & ((1ull << lane) - 1));
+    if (blockIdx.x == 0 && blockIdx.y == 0 && wave == 0) {
+      if (lane < p.k) store_choice(p, 0, lane, chosen, weight);
+      if (lane == 0) p.slots[0] = n;
+      if (local >> lane & 1) {
+        int *s = p.slots + 1 + 3 * slot;
+        s[0] = le;
+        s[1] = slot;
+        s[2] = 1;
+        p.pairs[slot] = lane;
+      }
+    }
+    if ((int)blockIdx.y >= n) return;
+    pair = __ffsll((unsigned long long)__ballot((local >> lane & 1) && slot == (int)blockIdx.y)) - 1;
+    e = __builtin_amdgcn_readlane(le, pair);
+    start = 0;
+    cnt = 1;
+  } else {
+    const int n = p.slots[0];
+    e = p.slots[1 + 3 * blockIdx.y];
+    start = p.slots[2 + 3 * blockIdx.y];
+    cnt = p.slots[3 + 3 * blockIdx.y];
+    if ((int)blockIdx.y >= n) return;
+  }
   const int c = lane & 7, q = lane >> 4, at = ((lane >> 3) & 1) * 32 + q * 8;
   const int i0 = (blockIdx.x * kWaves + wave) / share * 8, sub = wave & (share - 1);
   const int row = tile_row(i0, p.I) + c < p.I ? tile_row(i0, p.I) + c : p.I - 1;
@@ -326,7 +386,8 @@ __global__ __launch_bounds__(64 * kWaves, NT == 1 ? 6 : 4) void k_moe_gate_up(Mo
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       const int i = t0 + 8 * t + c;
-      x[t] = i < cnt ? (uint32_t)(p.pairs[start + i] / p.k * (int)p.ldx + at) * 2 : kNoColumn;
+      const int token = ONE > 0 ? 0 : i < cnt ? p.pairs[start + i] / p.k : 0;
+      x[t] = i < cnt ? (uint32_t)(token * (int)p.ldx + at) * 2 : kNoColumn;
     }
     f32x4 ag[NT] = {}, au[NT] = {};
     int s = lo;
@@ -398,8 +459,11 @@ __global__ __launch_bounds__(64 * kWaves, NT == 1 ? 6 : 4) void k_moe_gate_up(Mo
       }
       const int i = tile_row(ti, p.I) + r;
       const float a = i >= ti && i < p.I ? gs * sigma_f(gs) * us : 0.0f;  // zero in a repeated row's place
-      const uint16_t h = T::r(a);
-      uint16_t *out = p.a + p.pairs[start + t0 + tok] * p.lda * 2 + r;
+      uint16_t h = T::r(a);
+      // past the stored type's range the first part stays at its largest value:
+      // as an infinity it would cancel against the second's into a NaN
+      if ((h & 0x7fffu) == kInfBits<T>) h -= 1;
+      uint16_t *out = p.a + (ONE > 0 ? pair : p.pairs[start + t0 + tok]) * p.lda * 2 + r;
       out[a_at(ti)] = h;
       out[a_at(ti) + 64] = T::r(a - T::f(h));
       if (ti + 8 >= p.I)  // the last tile: zeros up to lda
@@ -639,13 +703,20 @@ hipError_t gate_up_s(const MoeParams &p, hipStream_t s) {
   const int slots = p.M * p.k < p.El ? p.M * p.k : p.El;  // at most this many experts have tokens
   const dim3 g((p.I + rows - 1) / rows, slots), b(64 * kWaves);
   const bool once = line_rows(p.w_gate, p.ld_wg, p.st_wg) && line_rows(p.w_up, p.ld_wu, p.st_wu);
+  if (moe_one(p)) {
+    if (p.E <= 128 && once) dgf_launch((k_moe_gate_up<T, 1, SHARE, true, false, 2>), g, b, 0, s, p);
+    else if (p.E <= 128) dgf_launch((k_moe_gate_up<T, 1, SHARE, false, false, 2>), g, b, 0, s, p);
+    else if (once) dgf_launch((k_moe_gate_up<T, 1, SHARE, true, false, 4>), g, b, 0, s, p);
+    else dgf_launch((k_moe_gate_up<T, 1, SHARE, false, false, 4>), g, b, 0, s, p);
+    return hipGetLastError();
+  }
   switch (token_tiles(p) * 2 + once) {
-    case 2: dgf_launch((k_moe_gate_up<T, 1, SHARE, false, false>), g, b, 0, s, p); break;
-    case 3: dgf_launch((k_moe_gate_up<T, 1, SHARE, true, false>), g, b, 0, s, p); break;
-    case 4: dgf_launch((k_moe_gate_up<T, 2, SHARE, false, false>), g, b, 0, s, p); break;
-    case 5: dgf_launch((k_moe_gate_up<T, 2, SHARE, true, false>), g, b, 0, s, p); break;
-    case 8: dgf_launch((k_moe_gate_up<T, 4, SHARE, false, false>), g, b, 0, s, p); break;
-    default: dgf_launch((k_moe_gate_up<T, 4, SHARE, true, false>), g, b, 0, s, p); break;
+    case 2: dgf_launch((k_moe_gate_up<T, 1, SHARE, false, false, 0>), g, b, 0, s, p); break;
+    case 3: dgf_launch((k_moe_gate_up<T, 1, SHARE, true, false, 0>), g, b, 0, s, p); break;
+    case 4: dgf_launch((k_moe_gate_up<T, 2, SHARE, false, false, 0>), g, b, 0, s, p); break;
+    case 5: dgf_launch((k_moe_gate_up<T, 2, SHARE, true, false, 0>), g, b, 0, s, p); break;
+    case 8: dgf_launch((k_moe_gate_up<T, 4, SHARE, false, false, 0>), g, b, 0, s, p); break;
+    default: dgf_launch((k_moe_gate_up<T, 4, SHARE, true, false, 0>), g, b, 0, s, p); break;
   }
   return hipGetLastError();
 }
@@ -655,7 +726,7 @@ template <class T>
 hipError_t gate_up_t(const MoeParams &p, hipStream_t s) {
   if (p.H < 8) {
     const dim3 g((p.I + 63) / 64, p.M * p.k < p.El ? p.M * p.k : p.El);
-    dgf_launch((k_moe_gate_up<T, 1, 1, false, true>), g, dim3(64 * kWaves), 0, s, p);
+    dgf_launch((k_moe_gate_up<T, 1, 1, false, true, 0>), g, dim3(64 * kWaves), 0, s, p);
     return hipGetLastError();
   }
   const int steps = p.H / 64;

@@ -155,6 +155,8 @@ def test_binding_refusals():
         binding.norm_fwd(f, w_next=w)
     with pytest.raises(ValueError, match="GPU tensor"):
         binding.norm_fwd(b, w_next=w)
+    with pytest.raises(ValueError, match="expanded"):
+        binding._gate(w.expand(4, 64), 4, 64, b)
     with pytest.raises(ValueError, match="rstd"):
         binding.norm_bwd(b, None, b)
     with pytest.raises(ValueError, match="GPU tensor"):

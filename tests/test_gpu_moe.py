@@ -98,7 +98,9 @@ def check(args, k, renorm, dt, lo=0, n=None):
 CASES = [(1, 64, 64, 4, 1, True), (1, 256, 128, 8, 2, True), (3, 8, 8, 3, 3, False), (5, 1003, 141, 60, 4, False),
          (9, 129, 77, 16, 8, True), (17, 512, 96, 5, 2, True), (32, 200, 200, 128, 8, True), (4, 1, 1, 2, 1, True),
          (64, 72, 40, 3, 1, False), (128, 136, 72, 20, 16, True), (128, 64, 64, 1, 1, True), (40, 96, 1000, 7, 7, False),
-         (2, 2048, 768, 16, 8, True), (1, 65, 3001, 9, 3, True), (7, 96, 33, 1024, 5, True)]
+         (2, 2048, 768, 16, 8, True), (1, 65, 3001, 9, 3, True), (7, 96, 33, 1024, 5, True),
+         (1, 96, 40, 200, 8, False), (1, 96, 40, 600, 4, True), (1, 8, 9, 129, 16, True), (33, 64, 24, 200, 3, False),
+         (100, 40, 16, 1000, 2, True), (128, 4096, 8, 1024, 16, True)]
 
 
 @pytest.mark.parametrize("dt", [BF, FH])
@@ -116,6 +118,28 @@ def test_ties_go_to_the_lowest_index():
     assert ids[2].tolist()[:4] == [3, 9, 70, 150]
     assert ids[4].tolist() == [0, 1, 2, 3, 4, 5]
     assert torch.equal(p[4], torch.full((6,), 1 / 6, dtype=torch.float32, device="cuda"))
+
+
+def test_activations_past_the_range_of_fp16():
+    # a of about 90000 (past 65504) times small down weights: y is finite and as exact as ever
+    x, wr, wg, wu, wd = make(3, 64, 32, 4, FH, seed=11)
+    x.fill_(1.0)
+    wg.fill_(300.0 / 64)
+    wu.fill_(300.0 / 64)
+    wd.mul_(2.0 ** -6)
+    y, _, p = dgf.moe_fwd(x, wr, wg, wu, wd, 1, routing=True)
+    ids = dgf.moe_fwd(x, wr, wg, wu, wd, 1, routing=True)[1]
+    g = float(f64(wg[0, 0, 0])) * 64
+    for m in range(3):
+        want = f64(wd[ids[m, 0]]).sum(1) * (g * g)
+        size = f64(wd[ids[m, 0]]).abs().sum(1) * (g * g)
+        assert torch.isfinite(y[m]).all()
+        # one rounding of y, and a's 22 bits and the sums' roundings of the terms
+        assert ((f64(y[m]) - want).abs() <= U[FH] * want.abs() + 32 * 2.0 ** -22 * size).all()
+    # far past it: infinities of the products' signs, never NaN
+    wg.fill_(30000.0 / 64)
+    y = dgf.moe_fwd(x, wr, wg, wu, wd.abs(), 1)
+    assert (y == float("inf")).all()
 
 
 def test_experts_without_tokens_are_not_read():
@@ -145,6 +169,16 @@ def test_shards_of_the_experts(dt):
     y = parts[1][0]
     none = ~(ids == 4).any(1)
     assert none.any() and (y[none].cpu().view(torch.int16) == 0).all()
+
+
+def test_shards_of_the_experts_for_one_token():
+    args = make(1, 192, 80, 10, BF, seed=9)
+    whole = check(args, 3, False, BF)
+    parts = [check(args, 3, False, BF, lo, 1) for lo in range(10)]
+    chosen = set(whole[1].flatten().tolist())
+    for e, (y, ids, p) in enumerate(parts):
+        assert torch.equal(ids, whole[1]) and torch.equal(p, whole[2])
+        assert bool((y.cpu().view(torch.int16) == 0).all()) == (e not in chosen)
 
 
 @pytest.mark.parametrize("H,I,E,k", [(512, 128, 16, 2), (192, 320, 24, 8), (100, 60, 6, 1)])
