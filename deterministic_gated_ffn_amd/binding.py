@@ -143,9 +143,10 @@ def _mat(t: torch.Tensor, name: str):
         raise TypeError(f"{name}: expected bfloat16 or float16, got {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name}: expected a GPU tensor")
-    if t.dim() != 2 or t.stride(1) != 1:
+    stride = t.stride()
+    if len(stride) != 2 or stride[1] != 1:
         raise ValueError(f"{name}: expected a 2-D row-major view (stride(1) == 1)")
-    return t.data_ptr(), t.stride(0)
+    return t.data_ptr(), stride[0]
 
 
 def _empty(rows: int, cols: int, like: torch.Tensor, ld: int | None = None) -> torch.Tensor:
@@ -371,22 +372,22 @@ def _vec(t, H: int, like: torch.Tensor, name: str):
     """Pointer of a contiguous [H] vector of like's dtype (None: NULL)."""
     if t is None:
         return None
+    if t.dtype is like.dtype and t.get_device() == like.get_device() and t.shape == (H,) and t.is_contiguous():
+        return t.data_ptr()
     if t.dtype != like.dtype or t.device != like.device:
         raise TypeError(f"{name}: expected {like.dtype} on {like.device}, got {t.dtype} on {t.device}")
-    if t.dim() != 1 or t.shape[0] != H or (H > 1 and t.stride(0) != 1):
-        raise ValueError(f"{name}: expected a contiguous vector of {H} elements")
-    return t.data_ptr()
+    raise ValueError(f"{name}: expected a contiguous vector of {H} elements")
 
 
 def _rows(t, shape, like: torch.Tensor, name: str):
     """(pointer, leading dimension) of a matrix of the given shape and like's dtype (None: NULL)."""
     if t is None:
         return None, 0
+    if t.dtype is like.dtype and t.get_device() == like.get_device() and t.shape == shape:
+        return _mat(t, name)
     if t.dtype != like.dtype or t.device != like.device:
         raise TypeError(f"{name}: expected {like.dtype} on {like.device}, got {t.dtype} on {t.device}")
-    if t.shape != shape:
-        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    return _mat(t, name)
+    raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
 def _gate(gate, M: int, H: int, like: torch.Tensor):
@@ -450,25 +451,31 @@ def norm_bwd(dz, dh, z, y=None, w_post=None, gate=None, alpha: float = 1.0, w_ne
     yp, ldy = _rows(y, (M, H), like, "y")
     gp, ldg = _gate(gate, M, H, like)
     wp, wn = _vec(w_post, H, like, "w_post"), _vec(w_next, H, like, "w_next")
-    if rstd.dtype != torch.float32 or tuple(rstd.shape) != (M, 2) or not rstd.is_contiguous() or rstd.device != like.device:
+    if (rstd.dtype is not torch.float32 or rstd.shape != (M, 2) or not rstd.is_contiguous()
+            or rstd.get_device() != like.get_device()):
         raise ValueError(f"rstd: expected the forward's contiguous float32 [{M}, 2]")
-    r = {}
     with _on(stream):
-        r["dres"] = _empty(M, H, like)
+        r = {"dres": _empty(M, H, like)}
+        dres, ld_dres = r["dres"].data_ptr(), r["dres"].stride(0)
+        dy = dw_post = dgate = dw_next = None
+        ld_dy = ld_dgate = 0
         if y is not None:
-            r["dy"] = _empty(M, H, like)
+            t = r["dy"] = _empty(M, H, like)
+            dy, ld_dy = t.data_ptr(), t.stride(0)
         if w_post is not None:
-            r["dw_post"] = torch.empty(H, dtype=like.dtype, device=like.device)
+            t = r["dw_post"] = torch.empty_like(w_post)
+            dw_post = t.data_ptr()
         if gate is not None:
-            r["dgate"] = torch.empty(H, dtype=like.dtype, device=like.device) if ldg == 0 else _empty(M, H, like)
+            t = r["dgate"] = torch.empty_like(gate) if ldg == 0 else _empty(M, H, like)
+            dgate, ld_dgate = t.data_ptr(), t.stride(0) if ldg else 0
         if w_next is not None:
-            r["dw_next"] = torch.empty(H, dtype=like.dtype, device=like.device)
-        ws = _workspace(L.dgf_norm_bwd_workspace(M, H), like)
-    ptr = {k: t.data_ptr() for k, t in r.items()}
-    _check(L.dgf_norm_bwd(dzp, lddz, dhp, lddh, zp, ldz, yp, ldy, wp, gp, ldg, alpha, wn, rstd.data_ptr(),
-                          ptr["dres"], r["dres"].stride(0), ptr.get("dy"), r["dy"].stride(0) if y is not None else 0,
-                          ptr.get("dw_post"), ptr.get("dgate"), r["dgate"].stride(0) if ldg else 0,
-                          ptr.get("dw_next"), M, H, ws.data_ptr(), ws.numel(), dt, _stream(stream)), "dgf_norm_bwd")
+            t = r["dw_next"] = torch.empty_like(w_next)
+            dw_next = t.data_ptr()
+        nbytes = L.dgf_norm_bwd_workspace(M, H)
+        ws = _workspace(nbytes, like)
+    _check(L.dgf_norm_bwd(dzp, lddz, dhp, lddh, zp, ldz, yp, ldy, wp, gp, ldg, alpha, wn, rstd.data_ptr(), dres, ld_dres,
+                          dy, ld_dy, dw_post, dgate, ld_dgate, dw_next, M, H, ws.data_ptr(), nbytes, dt, _stream(stream)),
+           "dgf_norm_bwd")
     return r
 
 
@@ -491,19 +498,21 @@ def _packed(M: int, N: int, like: torch.Tensor) -> Packed8:
     return Packed8(codes if ld == N else codes[:, :N], scales, like.dtype)
 
 
-def _q8(p: Packed8, shape, dtype, device, name: str):
+def _q8(p: Packed8, shape, dtype, device: int, name: str):
     """(codes, their leading dimension, scales, theirs) of a checkpoint of the given shape and type."""
-    q, s = p.codes, p.scales
+    q, s, stored = p
+    if stored is not dtype or q.dtype is not torch.int8 or s.dtype is not torch.float32:
+        raise TypeError(f"{name}: expected an 8-bit checkpoint of {dtype} (int8 codes, float32 scales)")
+    if device < 0 or q.get_device() != device or s.get_device() != device:
+        raise ValueError(f"{name}: expected GPU tensors of one device")
     M, N = shape
-    if p.dtype != dtype or q.dtype != torch.int8 or s.dtype != torch.float32 or q.device != device or s.device != device:
-        raise TypeError(f"{name}: expected an 8-bit checkpoint of {dtype} on {device} (int8 codes, float32 scales)")
-    if not q.is_cuda:
-        raise ValueError(f"{name}: expected GPU tensors")
-    if q.shape != (M, N) or s.shape != (M, -(-N // BLOCK8)):
+    blocks = -(-N // BLOCK8)
+    if q.shape != shape or s.shape != (M, blocks):
         raise ValueError(f"{name}: codes {tuple(q.shape)} and scales {tuple(s.shape)} are not those of a {M} x {N} matrix")
-    if (N > 1 and q.stride(1) != 1) or (s.shape[1] > 1 and s.stride(1) != 1):
+    qs, ss = q.stride(), s.stride()
+    if (N > 1 and qs[1] != 1) or (blocks > 1 and ss[1] != 1):
         raise ValueError(f"{name}: expected row-major codes and scales")
-    return q.data_ptr(), q.stride(0), s.data_ptr(), s.stride(0)
+    return q.data_ptr(), qs[0], s.data_ptr(), ss[0]
 
 
 def pack8(t, stream=None) -> Packed8:
@@ -525,7 +534,7 @@ def unpack8(p: Packed8, stream=None) -> torch.Tensor:
     if p.dtype not in _STORED:
         raise TypeError(f"expected a checkpoint of bfloat16 or float16, got {p.dtype}")
     M, N = p.codes.shape
-    qp, ldq, sp, lds = _q8(p, (M, N), p.dtype, p.codes.device, "p")
+    qp, ldq, sp, lds = _q8(p, (M, N), p.dtype, p.codes.get_device(), "p")
     with _on(stream):
         t = p.codes.new_empty((M, (N + 7) // 8 * 8), dtype=p.dtype)
         t = t if t.shape[1] == N else t[:, :N]
@@ -540,8 +549,8 @@ def act_bwd_q8(da, g: Packed8, u: Packed8, stream=None):
     dt = _stored(da)
     M, N = da.shape
     dap, ldda = _mat(da, "da")
-    gq, ldq, gs, lds = _q8(g, (M, N), da.dtype, da.device, "g")
-    uq, ldq2, us, lds2 = _q8(u, (M, N), da.dtype, da.device, "u")
+    gq, ldq, gs, lds = _q8(g, (M, N), da.dtype, da.get_device(), "g")
+    uq, ldq2, us, lds2 = _q8(u, (M, N), da.dtype, da.get_device(), "u")
     if (ldq, lds) != (ldq2, lds2):
         raise ValueError("g and u must share their leading dimensions")
     with _on(stream):
@@ -579,8 +588,8 @@ def ffn_bwd_q8(dy, x, g: Packed8, u: Packed8, w_gate, w_up, w_down, stream=None)
     dyp, lddy = _rows(dy, (M, H), x, "dy"); xp, ldx = _mat(x, "x")
     wg, ldwg = _rows(w_gate, (I, H), x, "w_gate"); wu, ldwu = _rows(w_up, (I, H), x, "w_up")
     wd, ldwd = _rows(w_down, (H, I), x, "w_down")
-    gq, ldq, gs, lds = _q8(g, (M, I), x.dtype, x.device, "g")
-    uq, ldq2, us, lds2 = _q8(u, (M, I), x.dtype, x.device, "u")
+    gq, ldq, gs, lds = _q8(g, (M, I), x.dtype, x.get_device(), "g")
+    uq, ldq2, us, lds2 = _q8(u, (M, I), x.dtype, x.get_device(), "u")
     if (ldq, lds) != (ldq2, lds2):
         raise ValueError("g and u must share their leading dimensions")
     with _on(stream):
@@ -595,13 +604,14 @@ def ffn_bwd_q8(dy, x, g: Packed8, u: Packed8, w_gate, w_up, w_down, stream=None)
 
 def _experts(t: torch.Tensor, shape, like: torch.Tensor, name: str):
     """(pointer, leading dimension, expert stride) of the experts' matrices [El, rows, cols]."""
-    if t.dtype != like.dtype or t.device != like.device:
+    if t.dtype is not like.dtype or t.get_device() != like.get_device():
         raise TypeError(f"{name}: expected {like.dtype} on {like.device}, got {t.dtype} on {t.device}")
     if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.stride(2) != 1:
+    stride = t.stride()
+    if stride[2] != 1:
         raise ValueError(f"{name}: expected row-major matrices (stride(2) == 1)")
-    return t.data_ptr(), t.stride(1), t.stride(0)
+    return t.data_ptr(), stride[1], stride[0]
 
 
 def moe_fwd(x, w_router, w_gate, w_up, w_down, top_k: int, renorm: bool = True, routing: bool = False,
@@ -625,12 +635,13 @@ def moe_fwd(x, w_router, w_gate, w_up, w_down, top_k: int, renorm: bool = True, 
     with _on(stream):
         y = _empty(M, H, x)
         if routing:
-            ids = torch.empty((M, max(top_k, 0)), dtype=torch.int32, device=x.device)
-            probs = torch.empty((M, max(top_k, 0)), dtype=torch.float32, device=x.device)
-        ws = _workspace(L.dgf_moe_fwd_workspace(M, H, I, E, El, top_k), x)
+            ids = x.new_empty((M, max(top_k, 0)), dtype=torch.int32)
+            probs = x.new_empty((M, max(top_k, 0)), dtype=torch.float32)
+        nbytes = L.dgf_moe_fwd_workspace(M, H, I, E, El, top_k)
+        ws = _workspace(nbytes, x)
     _check(L.dgf_moe_fwd(xp, ldx, wr, ldr, wg, ldg, sg, wu, ldu, su, wd, ldd, sd, y.data_ptr(), y.stride(0),
                          ids.data_ptr() if routing else None, probs.data_ptr() if routing else None,
-                         M, H, I, E, expert_offset, El, top_k, int(renorm), ws.data_ptr(), ws.numel(), dt,
+                         M, H, I, E, expert_offset, El, top_k, int(renorm), ws.data_ptr(), nbytes, dt,
                          _stream(stream)), "dgf_moe_fwd")
     return (y, ids, probs) if routing else y
 
