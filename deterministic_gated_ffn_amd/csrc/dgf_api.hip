@@ -487,10 +487,9 @@ dgf_status ffn_fwd_impl(int fmt, const void *x, int64_t ldx, const void *w_gate,
     f.g = (uint16_t *)g_save; f.u = (uint16_t *)u_save; f.ldgu = ld_gu;
     f.M = M; f.N = I; f.K = H; f.L = leaves(H); f.fmt = fmt;
     DGF_TRY(hip_check(timed(s, "gate/up + act", [&] { return launch_gu_act(f, s); }), "gate/up + act"));
-    if (q8) {
-      DGF_TRY(hip_check(timed(s, "pack g", [&] { return launch_pack8(fmt, f.g, ld_gu, q8->g, M, I, s); }), "pack g"));
-      DGF_TRY(hip_check(timed(s, "pack u", [&] { return launch_pack8(fmt, f.u, ld_gu, q8->u, M, I, s); }), "pack u"));
-    }
+    if (q8)
+      DGF_TRY(hip_check(timed(s, "pack g, u", [&] { return launch_pack8_pair(fmt, f.g, f.u, ld_gu, q8->g, q8->u, M, I, s); }),
+                        "pack g, u"));
   } else {
     GemmParams p = blank(fmt);
     p.A[0] = p.A[1] = (const uint16_t *)x;

@@ -7,9 +7,13 @@
 // Every chosen expert's weights are read once, whatever number of tokens chose
 // it: 3 H I 16-bit values for 6 H I operations a token, so up to about a
 // hundred tokens an expert the layer is bound by the weights' way from HBM.
-// Four launches: the router's products, the choice and the experts' token
-// lists (one workgroup), the gate/up products with the activation, and the
-// down products with the weighted sum over a token's experts.
+// Launches: the router's products; the choice and the experts' token lists (one
+// workgroup; for one token part of the next launch, past 32 tokens two); the
+// gate/up products with the activation; the down products with the weighted sum
+// over a token's experts (a launch of its own where workgroups share a row).
+// Measured, BF16: 32 tokens over 8 of 128 experts of 768 x 2048 take 4.6 + 8.8 +
+// 119 + 62 + 4.6 us, the products 5.9 and 5.7 TB/s of weights; one token of them
+// 3.2 + 13.7 + 10.6 us, three launches long enough to start and drain.
 //
 // Products run on the matrix cores with FP32 accumulators, 8 weight rows and 8
 // tokens per 16 x 16 x 32 instruction: rows 0-7 and 8-15 of the first operand
@@ -316,8 +320,16 @@ __device__ __forceinline__ typename T::frag load_column(__amdgpu_buffer_rsrc_t r
 // The activation a leaves as two stored parts whose sum keeps twice the
 // stored type's bits, so that rounding it adds nothing to the output's own
 // rounding: [pair][64 of the first, 64 of the second, ...], so that a step of
-// the down kernel takes one whole line of each.  K of the down products is padded to lda with zeros, and a ragged last chunk of 8 holds its
-// values at the end, for weights read from I - 8 (see k_moe_down).
+// the down kernel takes one whole line of each.  K of the down products is
+// padded to lda with zeros, and a ragged last chunk of 8 holds its values at the
+// end, for weights read from I - 8 (see k_moe_down).
+//
+// Bound by HBM where weight rows start on 128-byte lines: 6.2 TB/s at 8 experts
+// of 12288 x 4096 and 8 tokens, 5.9 at 128 of 768 x 2048 and 32.  Off the lines
+// every line of a row is asked for twice (1.8 times the requests, 1.1 times the
+// bytes from HBM) and it reaches 4.2 to 5.3; past about 4 tokens an expert the
+// tokens' own lines take as many of a CU's misses as the weights' (4.2 at 8,
+// 3.5 at 16 tokens an expert).
 constexpr int kChunk = 2;
 
 // Magnitude bits of the stored type's infinity, one above its largest value.
@@ -479,8 +491,10 @@ __global__ __launch_bounds__(64 * kWaves, NT == 1 ? 6 : 4) void k_moe_gate_up(Mo
 // keep all waves busy.  A wave's steps (64 K of an expert's rows against 8 NT
 // of its tokens) form one stream over all its experts, and the loads run R
 // steps ahead of the products through it: 8 R RT KB of weights in flight per
-// workgroup.  Loads past the end of the stream
-// read one fixed line.
+// workgroup (R 6 to 18 measure the same: what bounds it are the lines a CU can
+// wait for, a's among them; without a's loads 128 experts of 2048 x 768 took 52
+// us, with them 72 at 8 rows a workgroup and 62 at 16).  Loads past the end of
+// the stream read one fixed line.  5.75 TB/s at 8 experts of 4096 x 12288.
 //
 // The weights' last ragged chunk of 8 is read from I - 8, against a's last
 // chunk with its values at the end and zeros before, and later chunks again

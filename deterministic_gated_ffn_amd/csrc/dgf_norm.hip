@@ -8,6 +8,9 @@
 // written once, 8 bytes an element against about 12 operations, so the kernels
 // are bound by HBM.  Everything between the loads and the stores is FP32; z and
 // h are each rounded once, h from the unrounded z.
+// Measured at 4096 x 4096, BF16, with a gate for each channel: forward 21.8 us,
+// 6.2 TB/s; backward 36.9 us, 5.5 TB/s, and 4.2 us for its column sums (a copy
+// of 2 GiB reaches 5.0 TB/s on the same card, one of 256 MiB 5.5).
 #include "dgf_block.hpp"
 #include "dgf_rows.hpp"
 

@@ -110,6 +110,8 @@ struct Q8Mat {
 };
 
 hipError_t launch_pack8(int fmt, const uint16_t *x, int64_t ldx, Q8Mat o, int64_t M, int64_t N, hipStream_t s);
+hipError_t launch_pack8_pair(int fmt, const uint16_t *g, const uint16_t *u, int64_t ld, Q8Mat g8, Q8Mat u8, int64_t M,
+                             int64_t N, hipStream_t s);
 hipError_t launch_unpack8(int fmt, Q8Mat x, uint16_t *o, int64_t ldo, int64_t M, int64_t N, hipStream_t s);
 struct ActQ8Params {
   const uint16_t *da;
