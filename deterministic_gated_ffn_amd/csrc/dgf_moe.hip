@@ -302,6 +302,7 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 // Rows of the token operand through a buffer descriptor: a lane whose column
 // has no token gives an offset past its range and costs no memory request.
+// Leading dimensions are below 2^23, so 128 rows of x stay below 2^31 bytes.
 constexpr uint32_t kNoColumn = 0x80000000u;
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t column_rsrc(const uint16_t *p, int64_t bytes) {
   return __builtin_amdgcn_make_buffer_rsrc((void *)p, (short)0, (int)bytes, 0x00020000);

@@ -221,6 +221,20 @@ def test_offsets_past_32_bits():
     assert torch.equal(dgf.moe_fwd(args[0], args[1], args[2], far(args[3]), far(args[4]), 2), want)
 
 
+@pytest.mark.parametrize("H", (64, 72))
+def test_tokens_as_far_apart_as_a_leading_dimension_goes(H):
+    # 128 tokens of the largest stride: their last byte lies just below 2^31
+    M, ld = 128, (1 << 23) - 8
+    args = make(M, H, 48, 8, BF, seed=9)
+    buf = torch.empty((M - 1) * ld + H, dtype=BF, device="cuda")
+    x = torch.as_strided(buf, (M, H), (ld, 1))
+    x.copy_(args[0])
+    assert torch.equal(dgf.moe_fwd(x, *args[1:], 2), dgf.moe_fwd(*args, 2))
+    far = torch.as_strided(buf, (2, H), (1 << 23, 1))
+    with pytest.raises(RuntimeError, match="limit"):
+        dgf.moe_fwd(far, *args[1:], 2)
+
+
 def test_layer_replays_from_a_hip_graph():
     x, *w = make(16, 256, 128, 16, BF, seed=8)
     side = torch.cuda.Stream()
