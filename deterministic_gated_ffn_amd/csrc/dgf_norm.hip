@@ -233,10 +233,11 @@ __global__ __launch_bounds__(kBwdThreads, V == 1 ? 4 : 2) void k_norm_bwd(NormBw
         float dh[8];
         row_widen<T>(cur.dh[v], dh);
         row_widen<T>(wn[v], f);
-        const float k = live ? r_z : 0.0f;
+        if (live)  // not by a factor of 0: the row repeated may hold infinities
+#pragma unroll
+          for (int e = 0; e < 8; ++e) an[v][e] = fmaf(dh[e], z[e] * r_z, an[v][e]);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          an[v][e] = fmaf(dh[e], z[e] * k, an[v][e]);
           const float dn = dh[e] * f[e];
           s[0] = fmaf(dn, z[e], s[0]);
           g0[v][e] = fmaf(r_z, dn, g0[v][e]);

@@ -259,3 +259,17 @@ def test_no_rows():
     b = dgf.norm_bwd(e["dz"], e["dh"], r["z"], e["y"], d["w_post"], d["gate"], 1.0, d["w_next"], r["rstd"])
     for k in ("dw_post", "dw_next", "dgate"):
         assert b[k].shape == (H,) and (b[k].cpu().view(torch.int16) == 0).all(), k
+
+
+@pytest.mark.parametrize("M,H", [(513, 64), (515, 256), (769, 1024), (1031, 200)])
+def test_an_infinite_gradient_in_the_last_row_stays_an_infinity(M, H):
+    # a workgroup of several row slots has some without a row here
+    gen = torch.Generator().manual_seed(M)
+    z, y, dz, dh = (rows(gen, (M, H), BF) for _ in range(4))
+    w = torch.ones(H, dtype=BF, device="cuda")
+    z[M - 1, 5], dh[M - 1, 5] = 1.0, float("inf")
+    rstd = dgf.norm_fwd(z, y, w_post=w, w_next=w, training=True)["rstd"]
+    rstd[:, 1] = 1.0 / torch.sqrt(z.float().square().mean(1) + 1e-6)
+    d = dgf.norm_bwd(dz, dh, z, y, w_post=w, w_next=w, rstd=rstd)
+    dw = f64(d["dw_next"])
+    assert dw[5] == float("inf") and torch.isfinite(dw[torch.arange(H) != 5]).all()
