@@ -149,11 +149,19 @@ __global__ __launch_bounds__(1024) void k_norm_fwd(NormFwdParams p) {
 // go to `part` once (FP32, added up by k_norm_wgrad in the order of the
 // workgroups, so results do not change from run to run).
 //
-// ALL: dz, dh, y and w_post are all given (no test of them in the loop).  It
-// loads the next row before this one's reduction for rows of up to 8192
-// (V <= 2); wider ones have no registers left for that.  WHOLE: H is a multiple
-// of 8 (no element-by-element ends, which cost registers too).
+// PARTS: what is given, where that is known here (no test of it in the loop).
+// The next row is then loaded before this one's reduction, for rows of up to
+// 8192 (V <= 2): with dz and dh alone 4096 x 6000 takes 28.5 us, both launches,
+// against 47 with the tests.  Wider rows leave no registers for a second one
+// and keep the weights in LDS (1548 x 9819, no gate: 63 us against 80 read from
+// L2 again for every row).  Up to 12288 (V = 3) the next row's dz and dh are
+// loaded where this row's are used up, before the reduction, and the rest chunk
+// by chunk as the outputs leave (the same: 58; 1500 x 8320: 36 against 46); with
+// V <= 2 that is slower than the tests alone (4096 x 6000: 52), with V = 4 it
+// spills.  WHOLE: H is a multiple of 8 (no element-by-element ends, which cost
+// registers too).
 enum { GATE_NONE = 0, GATE_ROW = 1, GATE_FULL = 2 };
+enum { PARTS_ANY = 0, PARTS_ALL = 1, PARTS_NEXT = 2, PARTS_POST = 3 };  // dz dh y w_post; dz dh; dz y w_post
 
 template <int V, int GATE>
 struct NormRow {
@@ -161,15 +169,19 @@ struct NormRow {
   float r_y, r_z;
 };
 
-template <class T, int V, int GATE, bool ALL, bool WHOLE>
+template <class T, int V, int GATE, int PARTS, bool WHOLE>
 __global__ __launch_bounds__(kBwdThreads, V == 1 ? 4 : 2) void k_norm_bwd(NormBwdParams p, int row_threads) {
   __shared__ float4 red[2][kBwdThreads / 64];
-  extern __shared__ float cols[];  // round8(H) column sums, when a workgroup holds several rows
-  constexpr bool AHEAD = ALL && V <= 2;
+  // round8(H) column sums, when a workgroup holds several rows; with V > 2 the
+  // weights, [w_post, w_next, gate][V][thread] chunks of 8
+  extern __shared__ __attribute__((aligned(16))) float cols[];
+  constexpr bool AHEAD = PARTS != PARTS_ANY && V <= 2, IN_PLACE = V == 3, WIDE = V > 2;
   const int H = (int)p.H;
   const float inv_h = 1.0f / (float)H;
   const uint4 zero = make_uint4(0, 0, 0, 0);
-  const bool has_dz = ALL || p.dz, has_dh = ALL || p.dh, has_y = ALL || p.y, has_post = ALL || p.w_post;
+  const bool has_dz = PARTS != PARTS_ANY || p.dz, has_dh = PARTS == PARTS_ANY ? p.dh != nullptr : PARTS != PARTS_POST;
+  const bool has_y = PARTS == PARTS_ANY ? p.y != nullptr : PARTS != PARTS_NEXT;
+  const bool has_post = PARTS == PARTS_ANY ? p.w_post != nullptr : PARTS != PARTS_NEXT;
   const int slots = blockDim.x / row_threads, slot = __builtin_amdgcn_readfirstlane(threadIdx.x / row_threads);
   const int tid = threadIdx.x - slot * row_threads;
   const int w0 = slot * (row_threads >> 6), waves = row_threads >> 6;
@@ -183,25 +195,36 @@ __global__ __launch_bounds__(kBwdThreads, V == 1 ? 4 : 2) void k_norm_bwd(NormBw
   auto col = [&](int v) { return (tid + v * row_threads) * 8; };
   float ap[V][8] = {}, an[V][8] = {}, ag[V][8] = {};
   uint4 wp[V], wn[V], wg[V];  // w_post, w_next and a broadcast gate
-  auto load = [&](int64_t m, NormRow<V, GATE> &r) {
+  // a chunk's parts that the row's sums alone need, and those its outputs need too
+  auto load_sums = [&](int64_t m, NormRow<V, GATE> &r, int v) {
+    const int c = col(v);
+    r.dz[v] = r.dh[v] = zero;
+    if (c >= H) return;
+    if (has_dz) r.dz[v] = ld(p.dz + m * p.ld_dz, c);
+    if (has_dh) r.dh[v] = ld(p.dh + m * p.ld_dh, c);
+  };
+  auto load_both = [&](int64_t m, NormRow<V, GATE> &r, int v) {
+    const int c = col(v);
+    r.z[v] = r.y[v] = zero;
+    if constexpr (GATE == GATE_FULL) r.gate[v] = zero;
+    if (c >= H) return;
+    if (has_dh) r.z[v] = ld(p.z + m * p.ld_z, c);
+    if (has_y) r.y[v] = ld(p.y + m * p.ld_y, c);
+    if constexpr (GATE == GATE_FULL) r.gate[v] = ld(p.gate + m * p.ld_gate, c);
+  };
+  auto load_r = [&](int64_t m, NormRow<V, GATE> &r) {
     r.r_y = p.rstd[2 * m];
     r.r_z = p.rstd[2 * m + 1];
+  };
+  auto load = [&](int64_t m, NormRow<V, GATE> &r) {
+    load_r(m, r);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int c = col(v);
-      r.dz[v] = r.dh[v] = r.z[v] = r.y[v] = zero;
-      if constexpr (GATE == GATE_FULL) r.gate[v] = zero;
-      if (c >= H) continue;
-      if (has_dz) r.dz[v] = ld(p.dz + m * p.ld_dz, c);
-      if (has_dh) {
-        r.dh[v] = ld(p.dh + m * p.ld_dh, c);
-        r.z[v] = ld(p.z + m * p.ld_z, c);
-      }
-      if (has_y) r.y[v] = ld(p.y + m * p.ld_y, c);
-      if constexpr (GATE == GATE_FULL) r.gate[v] = ld(p.gate + m * p.ld_gate, c);
+      load_sums(m, r, v);
+      load_both(m, r, v);
     }
   };
-  auto weights = [&](int v) {
+  auto fetch = [&](int v) {
     const int c = col(v);
     wp[v] = wn[v] = wg[v] = zero;
     if (c >= H) return;
@@ -209,9 +232,26 @@ __global__ __launch_bounds__(kBwdThreads, V == 1 ? 4 : 2) void k_norm_bwd(NormBw
     if (has_dh) wn[v] = ld(p.w_next, c);
     if constexpr (GATE == GATE_ROW) wg[v] = ld(p.gate, c);
   };
-  if constexpr (AHEAD)
+  uint4 *kept = reinterpret_cast<uint4 *>(cols) + threadIdx.x;  // each thread its own
+  auto weights = [&](int v) {
+    if constexpr (WIDE) {
+      wp[v] = kept[v * blockDim.x];
+      wn[v] = kept[(V + v) * blockDim.x];
+      if constexpr (GATE == GATE_ROW) wg[v] = kept[(2 * V + v) * blockDim.x];
+    } else if constexpr (!AHEAD) {
+      fetch(v);
+    }
+  };
+  if constexpr (AHEAD || WIDE)
 #pragma unroll
-    for (int v = 0; v < V; ++v) weights(v);
+    for (int v = 0; v < V; ++v) {
+      fetch(v);
+      if constexpr (WIDE) {
+        kept[v * blockDim.x] = wp[v];
+        kept[(V + v) * blockDim.x] = wn[v];
+        if constexpr (GATE == GATE_ROW) kept[(2 * V + v) * blockDim.x] = wg[v];
+      }
+    }
   NormRow<V, GATE> cur, next;
   const int64_t step = (int64_t)gridDim.x * slots;
   // a slot past the last row repeats it and keeps nothing (its waves still meet the others at the barrier)
@@ -220,12 +260,13 @@ __global__ __launch_bounds__(kBwdThreads, V == 1 ? 4 : 2) void k_norm_bwd(NormBw
   int turn = 0;
   for (int64_t base = (int64_t)blockIdx.x * slots; base < p.M; base += step, m += step, turn ^= 1) {
     const bool live = m < p.M;
-    if constexpr (AHEAD) load(m + step < p.M ? m + step : p.M - 1, next);
+    const int64_t after = m + step < p.M ? m + step : p.M - 1;
+    if constexpr (AHEAD) load(after, next);
     const float r_y = cur.r_y, r_z = cur.r_z;
     float g0[V][8], s[3] = {0.0f, 0.0f, 0.0f};  // g0 = dz + r_z dn
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      if constexpr (!AHEAD) weights(v);
+      weights(v);
       float z[8], f[8];
       row_widen<T>(cur.dz[v], g0[v]);
       row_widen<T>(cur.z[v], z);
@@ -261,6 +302,11 @@ __global__ __launch_bounds__(kBwdThreads, V == 1 ? 4 : 2) void k_norm_bwd(NormBw
         }
       }
     }
+    if constexpr (IN_PLACE) {  // the next row's, where this one's are used up
+      load_r(after, cur);
+#pragma unroll
+      for (int v = 0; v < V; ++v) load_sums(after, cur, v);
+    }
     row_sums(s, red[turn], w0, waves);  // two sets in turn: no barrier between a row's reads and the next row's writes
     const float cz = has_dh ? r_z * r_z * r_z * (s[0] * inv_h) : 0.0f;
     const float cy = has_post ? r_y * r_y * r_y * ((s[1] - cz * s[2]) * inv_h) : 0.0f;
@@ -268,7 +314,7 @@ __global__ __launch_bounds__(kBwdThreads, V == 1 ? 4 : 2) void k_norm_bwd(NormBw
     for (int v = 0; v < V; ++v) {
       const int c = col(v);
       if (c >= H || !live) continue;
-      if constexpr (!AHEAD) weights(v);
+      weights(v);
       float z[8], o[8];
       row_widen<T>(cur.z[v], z);
 #pragma unroll
@@ -277,7 +323,10 @@ __global__ __launch_bounds__(kBwdThreads, V == 1 ? 4 : 2) void k_norm_bwd(NormBw
         o[e] = p.alpha * g0[v][e];
       }
       st(p.dres + m * p.ld_dres, c, row_narrow<T>(o));
-      if (!has_y) continue;
+      if (!has_y) {
+        if constexpr (IN_PLACE) load_both(after, cur, v);
+        continue;
+      }
       float y[8], w[8], f[8];
       row_widen<T>(cur.y[v], y);
 #pragma unroll
@@ -303,10 +352,11 @@ __global__ __launch_bounds__(kBwdThreads, V == 1 ? 4 : 2) void k_norm_bwd(NormBw
           g0[v][e] = fmaf(r_y * w[e], g0[v][e], -cy * y[e]);
         }
       }
+      if constexpr (IN_PLACE) load_both(after, cur, v);
       st(p.dy + m * p.ld_dy, c, row_narrow<T>(g0[v]));
     }
     if constexpr (AHEAD) cur = next;
-    else load(m + step < p.M ? m + step : p.M - 1, cur);
+    else if constexpr (!IN_PLACE) load(after, cur);
   }
   const int64_t ldp = (p.H + 7) & ~(int64_t)7;
 #pragma unroll
@@ -368,9 +418,11 @@ int row_threads(int64_t H, int V) {
 }
 
 // Chunks of 8 a backward thread: with two, half the reductions and no spilled
-// registers (4096 x 4096: 37 us against 48, 16384 x 1024: 41 against 45); below
-// 1024 a wave would be left half empty (3000 x 700: 29 us against 26).
-int bwd_chunks(int64_t H) { return H < 1024 ? 1 : H <= 16 * kBwdThreads ? 2 : 4; }
+// registers (4096 x 4096: 37 us against 49, 16384 x 1024: 40 against 45); below
+// 1024 a wave would be left half empty (3000 x 700: 24 us against 17).  Past 8192
+// as many as 512 threads need (1024 threads of two chunks spill: 113 us against
+// 80 at 1548 x 9819).
+int bwd_chunks(int64_t H) { return H < 1024 ? 1 : H <= 16 * kBwdThreads ? 2 : H <= 24 * kBwdThreads ? 3 : 4; }
 
 // Workgroups that fit the card at once: two a CU with V = 1, else one.
 int64_t bwd_most_groups(int64_t H) { return bwd_chunks(H) == 1 ? 512 : 256; }
@@ -414,11 +466,27 @@ template <class T, int V, int GATE>
 static void norm_bwd_v(const NormBwdParams &p, hipStream_t s) {
   const int rt = row_threads(p.H, V), slots = bwd_slots(p.M, p.H);
   const dim3 g((unsigned)p.groups), b(rt * slots);
-  const size_t lds = slots > 1 ? (size_t)((p.H + 7) & ~(int64_t)7) * 4 : 0;
-  const bool all = V <= 2 && p.dz && p.dh && p.y && p.w_post;
-  if (!all) dgf_launch((k_norm_bwd<T, V, GATE, false, false>), g, b, lds, s, p, rt);
-  else if (p.H % 8 == 0) dgf_launch((k_norm_bwd<T, V, GATE, true, true>), g, b, lds, s, p, rt);
-  else dgf_launch((k_norm_bwd<T, V, GATE, true, false>), g, b, lds, s, p, rt);
+  const size_t lds = V > 2 ? (size_t)(GATE == GATE_ROW ? 3 : 2) * V * rt * 16
+                   : slots > 1 ? (size_t)((p.H + 7) & ~(int64_t)7) * 4 : 0;
+  const bool whole = p.H % 8 == 0;
+  int parts = PARTS_ANY;
+  if (p.dz && p.dh && p.y && p.w_post) parts = PARTS_ALL;
+  else if (p.dz && p.dh && !p.y) parts = PARTS_NEXT;
+  else if (p.dz && !p.dh && p.y && p.w_post) parts = PARTS_POST;
+#define DGF_BWD(parts_, whole_) dgf_launch((k_norm_bwd<T, V, GATE, parts_, whole_>), g, b, lds, s, p, rt)
+  if constexpr (V <= 2) {
+    if constexpr (GATE == GATE_NONE)
+      if (parts == PARTS_NEXT) return whole ? DGF_BWD(PARTS_NEXT, true) : DGF_BWD(PARTS_NEXT, false);
+    if (parts == PARTS_ALL) return whole ? DGF_BWD(PARTS_ALL, true) : DGF_BWD(PARTS_ALL, false);
+    if (parts == PARTS_POST) return whole ? DGF_BWD(PARTS_POST, true) : DGF_BWD(PARTS_POST, false);
+    return DGF_BWD(PARTS_ANY, false);
+  } else {
+    // the tests cost less than the registers that the compiler spends without them, but for this
+    if constexpr (V == 3 && GATE != GATE_ROW)
+      if (parts == PARTS_ALL && whole) return DGF_BWD(PARTS_ALL, true);
+    return whole ? DGF_BWD(PARTS_ANY, true) : DGF_BWD(PARTS_ANY, false);
+  }
+#undef DGF_BWD
 }
 
 template <class T, int GATE>
@@ -426,6 +494,7 @@ static void norm_bwd_t(const NormBwdParams &p, hipStream_t s) {
   switch (bwd_chunks(p.H)) {
     case 1: norm_bwd_v<T, 1, GATE>(p, s); break;
     case 2: norm_bwd_v<T, 2, GATE>(p, s); break;
+    case 3: norm_bwd_v<T, 3, GATE>(p, s); break;
     default: norm_bwd_v<T, 4, GATE>(p, s); break;
   }
 }
