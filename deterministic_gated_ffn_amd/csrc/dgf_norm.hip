@@ -161,7 +161,8 @@ __global__ __launch_bounds__(1024) void k_norm_fwd(NormFwdParams p) {
 // spills.  WHOLE: H is a multiple of 8 (no element-by-element ends, which cost
 // registers too).
 enum { GATE_NONE = 0, GATE_ROW = 1, GATE_FULL = 2 };
-enum { PARTS_ANY = 0, PARTS_ALL = 1, PARTS_NEXT = 2, PARTS_POST = 3 };  // dz dh y w_post; dz dh; dz y w_post
+// dz, dh, y and w_post; dz and dh; dz, y and w_post; dh alone (the last norm of a network)
+enum { PARTS_ANY = 0, PARTS_ALL = 1, PARTS_NEXT = 2, PARTS_POST = 3, PARTS_LAST = 4 };
 
 template <int V, int GATE>
 struct NormRow {
@@ -179,9 +180,9 @@ __global__ __launch_bounds__(kBwdThreads, V == 1 ? 4 : 2) void k_norm_bwd(NormBw
   const int H = (int)p.H;
   const float inv_h = 1.0f / (float)H;
   const uint4 zero = make_uint4(0, 0, 0, 0);
-  const bool has_dz = PARTS != PARTS_ANY || p.dz, has_dh = PARTS == PARTS_ANY ? p.dh != nullptr : PARTS != PARTS_POST;
-  const bool has_y = PARTS == PARTS_ANY ? p.y != nullptr : PARTS != PARTS_NEXT;
-  const bool has_post = PARTS == PARTS_ANY ? p.w_post != nullptr : PARTS != PARTS_NEXT;
+  constexpr bool any = PARTS == PARTS_ANY, block = PARTS == PARTS_ALL || PARTS == PARTS_POST;
+  const bool has_dz = any ? p.dz != nullptr : PARTS != PARTS_LAST, has_dh = any ? p.dh != nullptr : PARTS != PARTS_POST;
+  const bool has_y = any ? p.y != nullptr : block, has_post = any ? p.w_post != nullptr : block;
   const int slots = blockDim.x / row_threads, slot = __builtin_amdgcn_readfirstlane(threadIdx.x / row_threads);
   const int tid = threadIdx.x - slot * row_threads;
   const int w0 = slot * (row_threads >> 6), waves = row_threads >> 6;
@@ -471,12 +472,14 @@ static void norm_bwd_v(const NormBwdParams &p, hipStream_t s) {
   const bool whole = p.H % 8 == 0;
   int parts = PARTS_ANY;
   if (p.dz && p.dh && p.y && p.w_post) parts = PARTS_ALL;
-  else if (p.dz && p.dh && !p.y) parts = PARTS_NEXT;
+  else if (p.dh && !p.y) parts = p.dz ? PARTS_NEXT : PARTS_LAST;
   else if (p.dz && !p.dh && p.y && p.w_post) parts = PARTS_POST;
 #define DGF_BWD(parts_, whole_) dgf_launch((k_norm_bwd<T, V, GATE, parts_, whole_>), g, b, lds, s, p, rt)
   if constexpr (V <= 2) {
-    if constexpr (GATE == GATE_NONE)
+    if constexpr (GATE == GATE_NONE) {
       if (parts == PARTS_NEXT) return whole ? DGF_BWD(PARTS_NEXT, true) : DGF_BWD(PARTS_NEXT, false);
+      if (parts == PARTS_LAST) return whole ? DGF_BWD(PARTS_LAST, true) : DGF_BWD(PARTS_LAST, false);
+    }
     if (parts == PARTS_ALL) return whole ? DGF_BWD(PARTS_ALL, true) : DGF_BWD(PARTS_ALL, false);
     if (parts == PARTS_POST) return whole ? DGF_BWD(PARTS_POST, true) : DGF_BWD(PARTS_POST, false);
     return DGF_BWD(PARTS_ANY, false);

@@ -276,19 +276,19 @@ def test_an_infinite_gradient_in_the_last_row_stays_an_infinity(M, H):
 
 
 @pytest.mark.parametrize("given,gate", [(a, b) for a in ("all", "no dz", "post") for b in ("none", "row", "full")]
-                         + [("next", "none")])  # without a block output there is no gate
+                         + [("next", "none"), ("last", "none")])  # without a block output there is no gate
 @pytest.mark.parametrize("M,H,dt", [(1100, 200, BF), (1100, 203, FH), (1031, 1024, FH), (520, 6001, BF), (520, 8200, BF),
                                     (520, 9819, FH), (530, 12288, FH), (300, 12296, BF), (300, 16379, FH)])
 def test_gradients_over_several_rows_a_workgroup(M, H, dt, gate, given):
     # every way of loading ahead, with the parts that may be missing
     d, e = make(M, H, dt, gate, True, seed=M + H)
-    drop = {"all": (), "no dz": ("dz",), "next": ("y", "w_post"), "post": ("dh", "w_next")}[given]
+    drop = {"all": (), "no dz": ("dz",), "next": ("y", "w_post"), "last": ("dz", "y", "w_post"),
+            "post": ("dh", "w_next")}[given]
     for k in drop:
         d[k] = e[k] = None
-    r = dgf.norm_fwd(d["res"], d["y"], d["w_post"], d["gate"], 0.75 if given != "next" else 1.0, d["w_next"], 1e-5,
-                     training=True)
+    alpha = 1.0 if d["y"] is None else 0.75
+    r = dgf.norm_fwd(d["res"], d["y"], d["w_post"], d["gate"], alpha, d["w_next"], 1e-5, training=True)
     rstd = f64(r["rstd"])
-    alpha = 0.75 if given != "next" else 1.0
     b = dgf.norm_bwd(d["dz"], d["dh"], r["z"], d["y"], d["w_post"], d["gate"], alpha, d["w_next"], r["rstd"])
     want, sizes = backward64(e["dz"], e["dh"], f64(r["z"]), e["y"], e["w_post"], e["gate"], alpha, e["w_next"],
                              rstd[:, :1], rstd[:, 1:])
