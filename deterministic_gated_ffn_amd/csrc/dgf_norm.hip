@@ -142,8 +142,10 @@ __global__ __launch_bounds__(1024) void k_norm_fwd(NormFwdParams p) {
 //   dy = r_y (dq - y r_y^2 mean(dq y))
 //
 // mean(dq y) is linear in G, so it follows from two sums that need no other
-// sum first: with q = gate w_post y, sum(G q) = sum((dz + r_z dn) q) - c sum(z q),
-// c = r_z^3 mean(dn z).  All three sums of a row take one reduction.  The
+// sum first: with n = z r_z and q = gate w_post y, sum(G q) = sum((dz + r_z dn) q)
+// - c sum(n q), c = r_z mean(dn n).  All three sums of a row take one reduction.
+// The normed row n, and y r_y below, take one factor r each: r^3 alone leaves
+// FP32's range for rows that do not (1e-45 at a root mean square of 1e15).  The
 // column sums dw_post, dw_next and a broadcast dgate stay in registers over
 // the workgroup's rows, then its row slots add up through LDS, in order, and
 // go to `part` once (FP32, added up by k_norm_wgrad in the order of the
@@ -275,9 +277,11 @@ __global__ __launch_bounds__(kBwdThreads, V == 1 ? 4 : 2) void k_norm_bwd(NormBw
         float dh[8];
         row_widen<T>(cur.dh[v], dh);
         row_widen<T>(wn[v], f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) z[e] *= r_z;
         if (live)  // not by a factor of 0: the row repeated may hold infinities
 #pragma unroll
-          for (int e = 0; e < 8; ++e) an[v][e] = fmaf(dh[e], z[e] * r_z, an[v][e]);
+          for (int e = 0; e < 8; ++e) an[v][e] = fmaf(dh[e], z[e], an[v][e]);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const float dn = dh[e] * f[e];
@@ -309,8 +313,8 @@ __global__ __launch_bounds__(kBwdThreads, V == 1 ? 4 : 2) void k_norm_bwd(NormBw
       for (int v = 0; v < V; ++v) load_sums(after, cur, v);
     }
     row_sums(s, red[turn], w0, waves);  // two sets in turn: no barrier between a row's reads and the next row's writes
-    const float cz = has_dh ? r_z * r_z * r_z * (s[0] * inv_h) : 0.0f;
-    const float cy = has_post ? r_y * r_y * r_y * ((s[1] - cz * s[2]) * inv_h) : 0.0f;
+    const float cz = has_dh ? r_z * (s[0] * inv_h) : 0.0f;
+    const float cy = has_post ? r_y * (r_y * ((s[1] - cz * s[2]) * inv_h)) : 0.0f;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int c = col(v);
@@ -320,7 +324,7 @@ __global__ __launch_bounds__(kBwdThreads, V == 1 ? 4 : 2) void k_norm_bwd(NormBw
       row_widen<T>(cur.z[v], z);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        g0[v][e] = fmaf(-cz, z[e], g0[v][e]);
+        g0[v][e] = fmaf(-cz, z[e] * r_z, g0[v][e]);
         o[e] = p.alpha * g0[v][e];
       }
       st(p.dres + m * p.ld_dres, c, row_narrow<T>(o));
@@ -349,8 +353,9 @@ __global__ __launch_bounds__(kBwdThreads, V == 1 ? 4 : 2) void k_norm_bwd(NormBw
       if (has_post) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          ap[v][e] = fmaf(g0[v][e], y[e] * r_y, ap[v][e]);
-          g0[v][e] = fmaf(r_y * w[e], g0[v][e], -cy * y[e]);
+          const float n = y[e] * r_y;
+          ap[v][e] = fmaf(g0[v][e], n, ap[v][e]);
+          g0[v][e] = fmaf(r_y * w[e], g0[v][e], -cy * n);
         }
       }
       if constexpr (IN_PLACE) load_both(after, cur, v);

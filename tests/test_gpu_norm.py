@@ -297,3 +297,31 @@ def test_gradients_over_several_rows_a_workgroup(M, H, dt, gate, given):
         close(k, b[k], want[k], sizes[k], dt, 128 if want[k].dim() == 2 else M / 512 + 256)
     again = dgf.norm_bwd(d["dz"], d["dh"], r["z"], d["y"], d["w_post"], d["gate"], alpha, d["w_next"], r["rstd"])
     assert all(torch.equal(b[k], again[k]) for k in b)
+
+
+@pytest.mark.parametrize("dz", [False, True])
+@pytest.mark.parametrize("M,H", [(4, 200), (4, 203), (5, 4096), (5, 9819), (4, 12288), (3, 16379)])
+def test_gradients_of_rows_far_from_one(M, H, dz):
+    """BF16 rows of root mean square 1e15 and 1e-13, and rows of zeros under an eps
+    of 1e-30 (r = 1e15): the cube of their r lies outside FP32, every term of the
+    formula within.  dh follows the normed row, so that the projection is no small
+    part of the gradient."""
+    gen = torch.Generator().manual_seed(H)
+    unit = torch.randn((3, M, H), generator=gen)
+    rms = torch.tensor([1e15, 1e-13, 1.0, 0.0, 1e15])[:M, None]
+    z, y = rows(gen, (M, H), BF), rows(gen, (M, H), BF)
+    z.copy_((unit[0] * rms).to(BF))
+    y.copy_((unit[1] * rms.flip(0)).to(BF))
+    dh = rows(gen, (M, H), BF)
+    dh.copy_((unit[0] + 0.5 * unit[2]).to(BF))
+    g = rows(gen, (M, H), BF, 0.1) if dz else None
+    w, wn, gate = rows(gen, (H,), BF, 0.1, 1.0), rows(gen, (H,), BF, 0.1, 1.0), rows(gen, (H,), BF, 0.3, 0.5)
+    rstd = torch.stack([(f64(t).square().mean(1) + 1e-30).rsqrt() for t in (y, z)], 1).float().cuda()
+    r_y, r_z = f64(rstd)[:, :1], f64(rstd)[:, 1:]
+    for yy, ww, gg in ((None, None, None), (y, w, None), (y, w, gate)):
+        b = dgf.norm_bwd(g, dh, z, yy, ww, gg, w_next=wn, rstd=rstd)
+        want, sizes = backward64(f64(g) if dz else None, f64(dh), f64(z), None if yy is None else f64(y),
+                                 None if ww is None else f64(w), None if gg is None else f64(gate), 1.0, f64(wn), r_y, r_z)
+        assert set(b) == set(want)
+        for k in want:
+            close(k, b[k], want[k], sizes[k], BF, 128 if want[k].dim() == 2 else 257)
