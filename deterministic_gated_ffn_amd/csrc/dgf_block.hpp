@@ -66,14 +66,14 @@ struct MoeParams {
   int *slots;                                // [1 + 3 min(El, M k)]: how many local experts have tokens, then of
                                              // each its index, its first entry in `pairs` and how many it has
   int *pairs;                                // [M k] (token, choice) pairs m k + j by slot, ascending within one
-  uint16_t *a;                               // [M k, 2 lda] the experts' activations in two parts, 8 and 8 in turn
+  uint16_t *a;                               // [M k, lda] the experts' activations, 32 bits each (dgf_moe.hip: put_a)
   int64_t lda;
   float *prod;                               // [M k, H] each pair's down product when split > 1, else null
   int row_tiles, split;                      // of the down kernel: 8 rows each per workgroup, workgroups per row tile
 };
 // Sets row_tiles and split from the sizes.
 void moe_plan(MoeParams &p);
-// Row length of one part of `a`: I rounded up to whole steps of the down kernel.
+// Columns of a row of `a`: I rounded up to whole steps of the down kernel.
 int64_t moe_down_ld(int I, int k);
 // Whether the gate/up kernel chooses the experts itself (no route launch).
 bool moe_one(const MoeParams &p);

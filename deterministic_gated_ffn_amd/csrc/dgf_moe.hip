@@ -318,12 +318,14 @@ __device__ __forceinline__ typename T::frag load_column(__amdgpu_buffer_rsrc_t r
 // 64, kChunk of them loaded together; the last of them also takes the ragged
 // rest), so that a wave has about 4 steps or more; 8 / share tiles a workgroup.
 //
-// The activation a leaves as two stored parts whose sum keeps twice the
-// stored type's bits, so that rounding it adds nothing to the output's own
-// rounding: [pair][64 of the first, 64 of the second, ...], so that a step of
-// the down kernel takes one whole line of each.  K of the down products is
-// padded to lda with zeros, and a ragged last chunk of 8 holds its values at the
-// end, for weights read from I - 8 (see k_moe_down).
+// The activation a leaves in 32 bits, two lines for every 64 columns of a pair,
+// so that a step of the down kernel takes both whole.  BF16: two stored parts
+// whose sum is a to 2^-16 of it, so that rounding it adds nothing to the
+// output's own rounding ([64 of the first, 64 of the second]).  FP16: the FP32
+// value itself ([4 of every 8, the other 4]), since parts in FP16 would lose a
+// past 2 x 65504 and, their second part a subnormal, below about 2^-3.  K of
+// the down products is padded to lda with zeros, and a ragged last chunk of 8
+// holds its values at the end, for weights read from I - 8 (see k_moe_down).
 //
 // Bound by HBM where weight rows start on 128-byte lines: 6.2 TB/s at 8 experts
 // of 12288 x 4096 and 8 tokens, 5.9 at 128 of 768 x 2048 and 32.  Off the lines
@@ -333,16 +335,48 @@ __device__ __forceinline__ typename T::frag load_column(__amdgpu_buffer_rsrc_t r
 // 3.5 at 16 tokens an expert).
 constexpr int kChunk = 2;
 
-// Magnitude bits of the stored type's infinity, one above its largest value.
+// Whether a passes between the kernels as FP32 values instead of two stored parts.
 template <class T>
-constexpr uint16_t kInfBits = T::code == Bf16::code ? 0x7f80 : 0x7c00;
+constexpr bool kWholeA = T::code == F16::code;
 
 // First row of the tile at i0: a ragged last tile takes the last 8 rows (the
 // first of them a second time).
 __device__ __forceinline__ int tile_row(int i0, int I) { return i0 + 8 <= I || I < 8 ? i0 : I - 8; }
 
-// Where column k of a pair's row has its first part (the second: 64 further on).
-__device__ __forceinline__ int a_at(int k) { return (k >> 6) * 128 + (k & 63); }
+// Column i of the chunk of 8 from column k, of a pair's row of a.
+template <class T>
+__device__ __forceinline__ void put_a(uint16_t *row, int k, int i, float a) {
+  if constexpr (kWholeA<T>) {
+    reinterpret_cast<float *>(row)[k - (k & 63) / 2 + i + 7 * (i & 4)] = a;
+  } else {
+    uint16_t h = T::r(a);
+    // past the stored type's range the first part stays at its largest value:
+    // as an infinity it would cancel against the second's into a NaN
+    if ((h & 0x7fffu) == 0x7f80u) h -= 1;
+    uint16_t *out = row + (k >> 6) * 128 + (k & 63) + i;
+    out[0] = h;
+    out[64] = T::r(a - T::f(h));
+  }
+}
+
+// acc + 8 weights a lane by the 8 columns of a beside them (a0, a1: a chunk as
+// its two lines hold it).  FP16 weights are exact in FP32, and so are their
+// products with FP32 a, four K an instruction: a sixteenth of the rate of FP16
+// products, which costs the down kernel 69 us against 62 at 32 tokens over 8 of
+// 128 experts of 768 x 2048, 54 against 43 at 64 over 8 of 16 of 1024 x 1024.
+template <class T>
+__device__ __forceinline__ f32x4 mul_a(const typename T::frag &w, const typename T::frag &a0,
+                                       const typename T::frag &a1, f32x4 acc) {
+  if constexpr (kWholeA<T>) {
+    const f32x4 lo = __builtin_bit_cast(f32x4, a0), hi = __builtin_bit_cast(f32x4, a1);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      acc = __builtin_amdgcn_mfma_f32_16x16x4f32((float)w[i], i < 4 ? lo[i] : hi[i - 4], acc, 0, 0, 0);
+    return acc;
+  } else {
+    return T::mfma(w, a1, T::mfma(w, a0, acc));
+  }
+}
 
 //
 // ONE > 0: a single token, whose choice (E <= 64 ONE) every workgroup makes for
@@ -472,15 +506,10 @@ __global__ __launch_bounds__(64 * kWaves, NT == 1 ? 6 : 4) void k_moe_gate_up(Mo
       }
       const int i = tile_row(ti, p.I) + r;
       const float a = i >= ti && i < p.I ? gs * sigma_f(gs) * us : 0.0f;  // zero in a repeated row's place
-      uint16_t h = T::r(a);
-      // past the stored type's range the first part stays at its largest value:
-      // as an infinity it would cancel against the second's into a NaN
-      if ((h & 0x7fffu) == kInfBits<T>) h -= 1;
-      uint16_t *out = p.a + (ONE > 0 ? pair : p.pairs[start + t0 + tok]) * p.lda * 2 + r;
-      out[a_at(ti)] = h;
-      out[a_at(ti) + 64] = T::r(a - T::f(h));
+      uint16_t *out = p.a + (ONE > 0 ? pair : p.pairs[start + t0 + tok]) * p.lda * 2;
+      put_a<T>(out, ti, r, a);
       if (ti + 8 >= p.I)  // the last tile: zeros up to lda
-        for (int k = ti + 8; k < p.lda; k += 8) out[a_at(k)] = out[a_at(k) + 64] = 0;
+        for (int k = ti + 8; k < p.lda; k += 8) put_a<T>(out, k, r, 0.0f);
     }
     __syncthreads();
   }
@@ -540,7 +569,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_moe_down(MoeParams p, int wps) 
   for (int i = 0; i < RT; ++i) wrow[i] = p.w_down + (h0 + 8 * i + c < p.H ? h0 + 8 * i + c : p.H - 1) * p.ld_wd;
 
   struct Step {
-    typename T::frag w[RT], hi[NT], lo[NT];
+    typename T::frag w[RT], a0[NT], a1[NT];
   };
   struct Cursor {
     int slot, t0, step, cnt, start, e;
@@ -574,8 +603,8 @@ __global__ __launch_bounds__(64 * kWaves) void k_moe_down(MoeParams p, int wps) 
     }
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      v.hi[t] = load_column<T>(ar, a[t] + ld.step * 256);
-      v.lo[t] = load_column<T>(ar, a[t] + ld.step * 256 + 128);
+      v.a0[t] = load_column<T>(ar, a[t] + ld.step * 256);
+      v.a1[t] = load_column<T>(ar, a[t] + ld.step * 256 + 128);
     }
     ld.step += go;
     if (ld.step < len) return;
@@ -613,10 +642,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_moe_down(MoeParams p, int wps) 
 #pragma unroll
           for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int i = 0; i < RT; ++i) {
-              acc[i][t] = T::mfma(ring[r].w[i], ring[r].hi[t], acc[i][t]);
-              acc[i][t] = T::mfma(ring[r].w[i], ring[r].lo[t], acc[i][t]);
-            }
+            for (int i = 0; i < RT; ++i) acc[i][t] = mul_a<T>(ring[r].w[i], ring[r].a0[t], ring[r].a1[t], acc[i][t]);
           if (++cu.step == len) {
 #pragma unroll
             for (int t = 0; t < NT; ++t) {

@@ -324,8 +324,8 @@ dgf_status dgf_ffn_bwd_q8(const void *dy, int64_t lddy, const void *x, int64_t l
  * The sum takes the experts this call holds; a token with none of them gets
  * y = +0, and the calls over all shards of the experts add up to the layer.
  * ids (int32) and probs (FP32), both [M,k] and optional, are the routing over
- * all E.  The products' sums and a's are FP32 (a passes between kernels with
- * twice the stored type's bits); y is rounded once.  Row m of every output
+ * all E.  The products' sums and a are FP32 (BF16 storage: a passes between the
+ * kernels to 2^-16 of its value); y is rounded once.  Row m of every output
  * depends on row m of x only, bit for bit, whatever M is, so more than 128
  * tokens can be given in pieces.
  * Weight rows that start on 128-byte lines (ld and strides multiples of 64) are

@@ -254,3 +254,34 @@ def test_layer_replays_from_a_hip_graph():
         torch.cuda.synchronize()
         for a, b in zip(out, eager):
             assert torch.equal(a, b), i
+
+
+@pytest.mark.parametrize("M", [1, 20])
+@pytest.mark.parametrize("gain,down", [(450.0, 2.0 ** -6), (30000.0, 2.0 ** -18), (4.5e-3, 100.0), (1e-3, 2e4)])
+def test_fp16_activations_of_any_size(M, gain, down):
+    """Activations of about 1e5, 6e8, 1e-5 and 5e-7 against down weights of both
+    signs that bring y back into FP16's normal range.  The tolerance is that of the
+    layer with a in FP32: its own 16 roundings, no bits lost between the kernels."""
+    H, I, E, k = 64, 100, 4, 2
+    gen = torch.Generator().manual_seed(M)
+    x, wr = rows(gen, (M, H), FH), rows(gen, (E, H), FH, H ** -0.5)
+    wg, wu = rows(gen, (E, I, H), FH, gain * H ** -0.5), rows(gen, (E, I, H), FH, gain * H ** -0.5)
+    wd = rows(gen, (E, H, I), FH, down * I ** -0.5)
+    y, ids, p = dgf.moe_fwd(x, wr, wg, wu, wd, k, routing=True)
+    y, p = f64(y), f64(p)
+    c1, c2 = 10 * (H / 64 + 1) + 16, 10 * (I / 64 + 1) + 16
+    want, size = torch.zeros(M, H, dtype=torch.float64), torch.zeros(M, H, dtype=torch.float64)
+    for m in range(M):
+        for j, e in enumerate(ids[m].tolist()):
+            G, W, D, xm = f64(wg[e]), f64(wu[e]), f64(wd[e]), f64(x[m])
+            g, u = G @ xm, W @ xm
+            a = g * torch.sigmoid(g) * u
+            aerr = 1.1 * c1 * EPS * (G.abs() @ xm.abs() * u.abs() + W.abs() @ xm.abs() * g.abs()) + 16 * EPS * a.abs()
+            want[m] += p[m, j] * (D @ a)
+            size[m] += p[m, j] * (D.abs() @ (aerr + c2 * EPS * a.abs()))
+    assert want.abs().max() < 60000 and want.norm() > 2.0 ** -14 * want.numel() ** 0.5
+    assert torch.isfinite(y).all()
+    off = (y - want).abs()
+    tol = U[FH] * want.abs() + size + 20 * EPS * want.abs() + 2.0 ** -25
+    assert (off <= tol).all(), f"{(off / tol).max():.3f} of the tolerance"
+    assert off.norm() <= U[FH] * want.norm()
