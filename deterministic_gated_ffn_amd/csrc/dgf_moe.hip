@@ -300,6 +300,15 @@ __device__ __forceinline__ typename T::frag load_weights(const uint16_t *p) {
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
+// 8 stored values with the first n zero (n <= 0: none, n >= 8: all).
+template <class F>
+__device__ __forceinline__ F drop_first(const F &v, int n) {
+  u32x4 b = __builtin_bit_cast(u32x4, v);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) b[j] &= n <= 2 * j ? 0xffffffffu : n == 2 * j + 1 ? 0xffff0000u : 0u;
+  return __builtin_bit_cast(F, b);
+}
+
 // Rows of the token operand through a buffer descriptor: a lane whose column
 // has no token gives an offset past its range and costs no memory request.
 // Leading dimensions are below 2^23, so 128 rows of x stay below 2^31 bytes.
@@ -347,6 +356,7 @@ __device__ __forceinline__ int tile_row(int i0, int I) { return i0 + 8 <= I || I
 template <class T>
 __device__ __forceinline__ void put_a(uint16_t *row, int k, int i, float a) {
   if constexpr (kWholeA<T>) {
+    asm volatile("" : "+v"(i));  // computed here, not kept over the caller's loop
     reinterpret_cast<float *>(row)[k - (k & 63) / 2 + i + 7 * (i & 4)] = a;
   } else {
     uint16_t h = T::r(a);
@@ -359,24 +369,37 @@ __device__ __forceinline__ void put_a(uint16_t *row, int k, int i, float a) {
   }
 }
 
-// acc + 8 weights a lane by the 8 columns of a beside them (a0, a1: a chunk as
-// its two lines hold it).  FP16 weights are exact in FP32, and so are their
-// products with FP32 a, four K an instruction: a sixteenth of the rate of FP16
-// products, which costs the down kernel 69 us against 62 at 32 tokens over 8 of
-// 128 experts of 768 x 2048, 54 against 43 at 64 over 8 of 16 of 1024 x 1024.
+// Sums of products of 8 weights a lane and the 8 columns of a beside them (a0,
+// a1: a chunk as its two lines hold it).  FP16 weights are exact in FP32, and so
+// are their products with FP32 a, four K an instruction: a sixteenth of the rate
+// of FP16 products, which costs the down kernel 69 us against 62 at 32 tokens
+// over 8 of 128 experts of 768 x 2048, 54 against 43 at 64 over 8 of 16 of 1024 x
+// 1024.  BF16: a sum for each part, so that where an infinite weight makes the
+// first an infinity, its product with the second (0, or of the other sign) is
+// left out.
 template <class T>
-__device__ __forceinline__ f32x4 mul_a(const typename T::frag &w, const typename T::frag &a0,
-                                       const typename T::frag &a1, f32x4 acc) {
-  if constexpr (kWholeA<T>) {
-    const f32x4 lo = __builtin_bit_cast(f32x4, a0), hi = __builtin_bit_cast(f32x4, a1);
+struct SumA {
+  f32x4 first, second;  // second: unused with FP32 a
+  __device__ __forceinline__ void clear() { first = second = f32x4{0.f, 0.f, 0.f, 0.f}; }
+  __device__ __forceinline__ void add(const typename T::frag &w, const typename T::frag &a0, const typename T::frag &a1) {
+    if constexpr (kWholeA<T>) {
+      const f32x4 lo = __builtin_bit_cast(f32x4, a0), hi = __builtin_bit_cast(f32x4, a1);
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      acc = __builtin_amdgcn_mfma_f32_16x16x4f32((float)w[i], i < 4 ? lo[i] : hi[i - 4], acc, 0, 0, 0);
-    return acc;
-  } else {
-    return T::mfma(w, a1, T::mfma(w, a0, acc));
+      for (int i = 0; i < 8; ++i)
+        first = __builtin_amdgcn_mfma_f32_16x16x4f32((float)w[i], i < 4 ? lo[i] : hi[i - 4], first, 0, 0, 0);
+    } else {
+      first = T::mfma(w, a0, first);
+      second = T::mfma(w, a1, second);
+    }
   }
-}
+  __device__ __forceinline__ f32x4 sum() const {
+    f32x4 v = first;
+    if constexpr (!kWholeA<T>)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = fabsf(v[i]) == INFINITY ? v[i] : v[i] + second[i];
+    return v;
+  }
+};
 
 //
 // ONE > 0: a single token, whose choice (E <= 64 ONE) every workgroup makes for
@@ -465,25 +488,26 @@ __global__ __launch_bounds__(64 * kWaves, NT == 1 ? 6 : 4) void k_moe_gate_up(Mo
       }
     }
     if (rest) {
-      // a chunk of 8 that would pass H is read from H - 8, x with zeros where
-      // the weight belongs to an earlier chunk
+      // a chunk of 8 that would pass H is read from H - 8, with zeros for what
+      // belongs to an earlier chunk (in both operands: either may be infinite)
       const int k = steps * 64 + at, from = k < p.H - 8 ? k : p.H - 8;
+      int drop = k - from;
+      asm volatile("" : "+v"(drop));  // its masks stay here: kept over the loop they cost 4 registers
       typename T::frag fg, fu;
-      if constexpr (SMALL) fg = load_frag_tail<T>(wg, k, p.H), fu = load_frag_tail<T>(wu, k, p.H);
-      else fg = load_weights<T, ONCE>(wg + from), fu = load_weights<T, ONCE>(wu + from);
+      if constexpr (SMALL) {
+        fg = load_frag_tail<T>(wg, k, p.H), fu = load_frag_tail<T>(wu, k, p.H);
+      } else {
+        fg = drop_first(load_weights<T, ONCE>(wg + from), drop);
+        fu = drop_first(load_weights<T, ONCE>(wu + from), drop);
+      }
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         const uint16_t *row = p.x + (x[t] < kNoColumn ? x[t] / 2 - at : 0);
-        u16x8 fx;
-        if constexpr (SMALL) {
-          fx = __builtin_bit_cast(u16x8, load_frag_tail<T>(row, k, p.H));
-        } else {
-          fx = __builtin_bit_cast(u16x8, load_weights<T, false>(row + from));
-#pragma unroll
-          for (int i = 0; i < 8; ++i) fx[i] = from + i >= k ? fx[i] : (uint16_t)0;
-        }
-        ag[t] = T::mfma(fg, __builtin_bit_cast(typename T::frag, fx), ag[t]);
-        au[t] = T::mfma(fu, __builtin_bit_cast(typename T::frag, fx), au[t]);
+        typename T::frag fx;
+        if constexpr (SMALL) fx = load_frag_tail<T>(row, k, p.H);
+        else fx = drop_first(load_weights<T, false>(row + from), drop);
+        ag[t] = T::mfma(fg, fx, ag[t]);
+        au[t] = T::mfma(fu, fx, au[t]);
       }
     }
 #pragma unroll
@@ -528,8 +552,9 @@ __global__ __launch_bounds__(64 * kWaves, NT == 1 ? 6 : 4) void k_moe_gate_up(Mo
 //
 // The weights' last ragged chunk of 8 is read from I - 8, against a's last
 // chunk with its values at the end and zeros before, and later chunks again
-// from there against zeros: no load passes a row's end.  (SMALL: I < 8, where
-// there is no such 8; element by element.)
+// from there against zeros: no load passes a row's end.  The weights that meet
+// those zeros are made zeros too (an infinity would make a NaN).  (SMALL: I < 8,
+// where there is no such 8; element by element.)
 //
 // Each (token, choice) pair's partial products stay in LDS and are added up in
 // order at the end: the waves' shares, then the choices by p.  Where the rows
@@ -634,25 +659,35 @@ __global__ __launch_bounds__(64 * kWaves) void k_moe_down(MoeParams p, int wps) 
     Step ring[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) load(ring[r]);
-    f32x4 acc[RT][NT] = {};
+    SumA<T> acc[RT][NT];
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+      for (int t = 0; t < NT; ++t) acc[i][t].clear();
     while (cu.slot < n) {
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         if (cu.slot < n) {
+          if (!SMALL && (sub * len + cu.step + 1) * 64 > p.I) {
+            // columns past I, and those of the last chunk that were read twice: as 0 x 0
+            const int past = k0 + cu.step * 64 - (p.I - 8);
+#pragma unroll
+            for (int i = 0; i < RT; ++i) ring[r].w[i] = drop_first(ring[r].w[i], past);
+          }
 #pragma unroll
           for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int i = 0; i < RT; ++i) acc[i][t] = mul_a<T>(ring[r].w[i], ring[r].a0[t], ring[r].a1[t], acc[i][t]);
+            for (int i = 0; i < RT; ++i) acc[i][t].add(ring[r].w[i], ring[r].a0[t], ring[r].a1[t]);
           if (++cu.step == len) {
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
               const int at_ = cu.t0 + 8 * t + c;
 #pragma unroll
               for (int i = 0; i < RT; ++i) {
-                const f32x4 v = diagonal(acc[i][t]);
+                const f32x4 v = diagonal(acc[i][t].sum());
                 if (lane < 32 && (lane & 8) == 0 && at_ < cu.cnt)
                   *reinterpret_cast<f32x4 *>(&part[(pairs[cu.start + at_] * wps + sub) * ROWS + 8 * i + q * 4]) = v;
-                acc[i][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+                acc[i][t].clear();
               }
             }
             cu.step = 0;

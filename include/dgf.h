@@ -329,8 +329,7 @@ dgf_status dgf_ffn_bwd_q8(const void *dy, int64_t lddy, const void *x, int64_t l
  * depends on row m of x only, bit for bit, whatever M is, so more than 128
  * tokens can be given in pieces.
  * Weight rows that start on 128-byte lines (ld and strides multiples of 64) are
- * read fastest.  Weights are taken as finite: an infinite one among the last 8
- * of a row whose length is no multiple of 64 may give NaN for an infinity.
+ * read fastest.
  * Limits: M <= 128, k <= 16, E <= 1024, I <= 131072 (else DGF_EUNSUPPORTED).  Workspace:
  * dgf_moe_fwd_workspace bytes.  M = 0: DGF_OK, no launch.
  */

@@ -285,3 +285,42 @@ def test_fp16_activations_of_any_size(M, gain, down):
     tol = U[FH] * want.abs() + size + 20 * EPS * want.abs() + 2.0 ** -25
     assert (off <= tol).all(), f"{(off / tol).max():.3f} of the tolerance"
     assert off.norm() <= U[FH] * want.norm()
+
+
+@pytest.mark.parametrize("dt", [BF, FH])
+@pytest.mark.parametrize("M,H,I,k", [(1, 64, 64, 2), (20, 72, 77, 2), (1, 1003, 192, 1), (33, 100, 768, 1), (9, 6, 5, 3),
+                                     (40, 520, 1411, 4)])
+def test_infinite_weights_give_infinities(M, H, I, k, dt):
+    """One infinite weight at a time, all else positive: y is that infinity where the
+    formula has it, and keeps its bits elsewhere.  Columns that are read twice or
+    padded, and the second part of a, must not make a NaN of it."""
+    E, inf = 6, float("inf")
+    gen = torch.Generator().manual_seed(M + H)
+    x, wr, wg, wu, wd = (rows(gen, s, dt, c).abs_().clamp_(min=2.0 ** -12) for s, c in (((M, H), 1.0), ((E, H), H ** -0.5), ((E, I, H), H ** -0.5),
+                                                                 ((E, I, H), H ** -0.5), ((E, H, I), I ** -0.5)))
+    base, ids, _ = dgf.moe_fwd(x, wr, wg, wu, wd, k, routing=True)
+    e = ids[0, 0].item()
+    hit = (ids == e).any(1).cpu()
+    assert (wd[e] > 0).all() and torch.isfinite(base).all()
+
+    def check_at(w, at, value, cols):
+        kept = w[at].clone()
+        w[at] = value
+        y = dgf.moe_fwd(x, wr, wg, wu, wd, k)
+        w[at] = kept
+        want = base.cpu().clone()
+        want[hit.nonzero(), torch.arange(H) if cols is None else torch.tensor([cols])] = value
+        assert torch.equal(y.cpu().view(torch.int16), want.view(torch.int16)), (at, value)
+
+    for w in (wg, wu):
+        for i in sorted({0, I // 2, I - 1}):
+            for h in sorted({0, H - 1, max(H - 8, 0)}):
+                check_at(w, (e, i, h), inf, None)
+    for i in sorted({0, I // 3, I // 2, max(I - 9, 0), max(I - 8, 0), max(I - 5, 0), I - 1}):
+        for h in (0, H - 1):
+            check_at(wd, (e, h, i), inf, h)
+            check_at(wd, (e, h, i), -inf, h)
+    if I > 1:  # one of each sign has no sum
+        wd[e, 0, 0], wd[e, 0, I - 1] = inf, -inf
+        y = dgf.moe_fwd(x, wr, wg, wu, wd, k).cpu()
+        assert torch.isnan(y[hit, 0]).all() and torch.equal(y[:, 1:], base.cpu()[:, 1:])
