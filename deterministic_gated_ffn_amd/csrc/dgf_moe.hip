@@ -78,9 +78,10 @@ __global__ __launch_bounds__(256) void k_moe_logits(MoeParams p) {
     p.logits[(int64_t)(m0 + t) * p.E + e] = ((red[0][t] + red[1][t]) + red[2][t]) + red[3][t];
 }
 
-// Order of logits as integers: larger float, larger integer; NaN lowest; never 0.
+// Order of logits as integers: larger float, larger integer, equal floats (-0
+// and +0 too) equal; NaN lowest; never 0.
 __device__ __forceinline__ uint32_t logit_key(float l) {
-  const uint32_t b = __float_as_uint(l);
+  const uint32_t b = l == 0.0f ? 0u : __float_as_uint(l);
   if ((b & 0x7fffffffu) > 0x7f800000u) return 1u;
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }

@@ -324,3 +324,16 @@ def test_infinite_weights_give_infinities(M, H, I, k, dt):
         wd[e, 0, 0], wd[e, 0, I - 1] = inf, -inf
         y = dgf.moe_fwd(x, wr, wg, wu, wd, k).cpu()
         assert torch.isnan(y[hit, 0]).all() and torch.equal(y[:, 1:], base.cpu()[:, 1:])
+
+
+@pytest.mark.parametrize("M", [1, 3, 40])
+def test_zero_logits_of_either_sign_tie(M):
+    # products of 2^-100 and -2^-100 round to -0 in FP32, products with 0 to +0
+    H, E, k = 2048, 6, 5
+    x, wr, wg, wu, wd = make(M, H, 16, E, BF, seed=12)
+    x.fill_(2.0 ** -100)
+    wr.fill_(0.0)
+    wr[0::2] = -2.0 ** -100
+    _, ids, p = dgf.moe_fwd(x, wr, wg, wu, wd, k, routing=True)
+    assert ids.tolist() == [[0, 1, 2, 3, 4]] * M
+    assert (p == p[0, 0]).all()
