@@ -325,3 +325,35 @@ def test_gradients_of_rows_far_from_one(M, H, dz):
         assert set(b) == set(want)
         for k in want:
             close(k, b[k], want[k], sizes[k], BF, 128 if want[k].dim() == 2 else 257)
+
+
+@pytest.mark.parametrize("given,gate", [("all", "none"), ("all", "row"), ("all", "full"), ("next", "none"),
+                                        ("post", "row"), ("plain", "row")])
+@pytest.mark.parametrize("M,H,dt", [(1031, 203, BF), (1100, 200, FH), (700, 1024, BF), (520, 4096, BF), (520, 6001, FH),
+                                    (520, 9819, BF), (530, 12288, BF), (300, 16379, FH), (300, 16384, BF)])
+def test_dres_written_over_dz(M, H, dt, gate, given):
+    # rows loaded ahead, rows repeated in slots without one, ragged ends: the same bits as apart
+    d, _ = make(M, H, dt, gate, given != "plain", seed=M)
+    if given == "next":
+        d["y"] = d["w_post"] = None
+    if given == "post":
+        d["dh"] = d["w_next"] = None
+    alpha = 1.0 if d["y"] is None else 0.75
+    r = dgf.norm_fwd(d["res"], d["y"], d["w_post"], d["gate"], alpha, d["w_next"], 1e-5, training=True)
+    want = dgf.norm_bwd(d["dz"], d["dh"], r["z"], d["y"], d["w_post"], d["gate"], alpha, d["w_next"], r["rstd"])
+    L = dgf.load()
+    out = {k: torch.empty_strided(v.shape, v.stride(), dtype=dt, device="cuda") for k, v in want.items() if k != "dres"}
+    dz = d["dz"]
+    nbytes = L.dgf_norm_bwd_workspace(M, H)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+    ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    ld = lambda t: 0 if t is None or t.dim() == 1 else t.stride(0)  # noqa: E731
+    st = L.dgf_norm_bwd(ptr(dz), ld(dz), ptr(d["dh"]), ld(d["dh"]), ptr(r["z"]), ld(r["z"]), ptr(d["y"]), ld(d["y"]),
+                        ptr(d["w_post"]), ptr(d["gate"]), ld(d["gate"]), alpha, ptr(d["w_next"]), ptr(r["rstd"]),
+                        ptr(dz), ld(dz), ptr(out.get("dy")), ld(out.get("dy")), ptr(out.get("dw_post")),
+                        ptr(out.get("dgate")), ld(out.get("dgate")), ptr(out.get("dw_next")), M, H, ptr(ws), nbytes,
+                        dgf.DGF_BF16 if dt == BF else dgf.DGF_FP16, torch.cuda.current_stream().cuda_stream)
+    assert st == 0, L.dgf_last_error()
+    assert torch.equal(dz, want["dres"])
+    for k in out:
+        assert torch.equal(out[k], want[k]), k
