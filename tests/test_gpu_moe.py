@@ -337,3 +337,18 @@ def test_zero_logits_of_either_sign_tie(M):
     _, ids, p = dgf.moe_fwd(x, wr, wg, wu, wd, k, routing=True)
     assert ids.tolist() == [[0, 1, 2, 3, 4]] * M
     assert (p == p[0, 0]).all()
+
+
+@pytest.mark.parametrize("dt", [BF, FH])
+@pytest.mark.parametrize("M,H,I,E,k", [(64, 136, 100, 128, 1), (128, 64, 72, 16, 1), (128, 136, 100, 4, 1), (40, 512, 77, 60, 3)])
+def test_most_tokens_on_one_expert(M, H, I, E, k, dt):
+    # far more tokens than a pass over an expert's weights takes, while the mean is small
+    x, wr, wg, wu, wd = make(M, H, I, E, dt, seed=13)
+    x.abs_()
+    wr[E // 2].abs_()
+    wr[E // 2].mul_(4.0)
+    y, ids, p = check((x, wr, wg, wu, wd), k, True, dt)
+    assert (ids[:, 0] == E // 2).sum() > 0.9 * M
+    for m in (0, 9, 17, M - 1):
+        for a, b in zip((y, ids, p), dgf.moe_fwd(x[m:m + 1], wr, wg, wu, wd, k, routing=True)):
+            assert torch.equal(a[m:m + 1], b), m
