@@ -4,16 +4,21 @@
 //   p = softmax of l over all E experts, or over the k chosen (renorm)
 //   a_j = silu(W_gate[e_j] x) (W_up[e_j] x);  y = sum_j p_j W_down[e_j] a_j
 //
-// Every chosen expert's weights are read once, whatever number of tokens chose
-// it: 3 H I 16-bit values for 6 H I operations a token, so up to about a
-// hundred tokens an expert the layer is bound by the weights' way from HBM.
+// Each chosen expert takes 3 H I 16-bit weights for 6 H I operations a token, so
+// the layer is bound by the weights' way from HBM up to about 4 tokens an expert;
+// with more, by the tokens' own lines and by reading weights again: one pass over
+// an expert's weights takes 8, 16 or 32 tokens (by the mean number that an expert
+// gets, token_tiles), and an expert that more tokens chose is passed over again.
+// With 8 of 128 experts of 768 x 2048 that costs 115 + 61 us in the products at 32
+// tokens and 181 + 105 at 128; all of 128 tokens on one expert 80 + 45 in 16
+// passes, 8 of them on it 7.6 + 7.3.
 // Launches: the router's products; the choice and the experts' token lists (one
 // workgroup; for one token part of the next launch, past 32 tokens two); the
 // gate/up products with the activation; the down products with the weighted sum
 // over a token's experts (a launch of its own where workgroups share a row).
 // Measured, BF16: 32 tokens over 8 of 128 experts of 768 x 2048 take 4.6 + 8.8 +
-// 119 + 62 + 4.6 us, the products 5.9 and 5.7 TB/s of weights; one token of them
-// 3.2 + 13.7 + 10.6 us, three launches long enough to start and drain.
+// 116 + 62 + 4.6 us, the products 5.9 and 5.7 TB/s of weights; one token of them
+// 3.0 + 13.2 + 10.8 us, three launches long enough to start and drain.
 //
 // Products run on the matrix cores with FP32 accumulators, 8 weight rows and 8
 // tokens per 16 x 16 x 32 instruction: rows 0-7 and 8-15 of the first operand
@@ -373,7 +378,7 @@ __device__ __forceinline__ void put_a(uint16_t *row, int k, int i, float a) {
 // Sums of products of 8 weights a lane and the 8 columns of a beside them (a0,
 // a1: a chunk as its two lines hold it).  FP16 weights are exact in FP32, and so
 // are their products with FP32 a, four K an instruction: a sixteenth of the rate
-// of FP16 products, which costs the down kernel 69 us against 62 at 32 tokens
+// of FP16 products, which costs the down kernel 70 us against 62 at 32 tokens
 // over 8 of 128 experts of 768 x 2048, 54 against 43 at 64 over 8 of 16 of 1024 x
 // 1024.  BF16: a sum for each part, so that where an infinite weight makes the
 // first an infinity, its product with the second (0, or of the other sign) is
@@ -763,7 +768,10 @@ int waves_per_slot(int k) {
 constexpr double kCombineBytes = 100e3, kStartBytes = 60e3;
 
 // Token tiles of 8 that one pass over an expert's weights takes, from the
-// mean number of tokens an expert gets.
+// mean number of tokens an expert gets.  Both products with 1 / 2 / 4 tiles, us:
+// 4 of 32 experts (1024 x 2048) at a mean of 4: 80 / 92 / 121, 8: 120 / 103 / 130,
+// 12: 157 / 118 / 140, 16: 206 / 163 / 151; 2 of 8 (4096 x 4096) at 4: 135 / 156 /
+// 212, 8: 189 / 177 / 230, 12: 295 / 231 / 248, 16: 381 / 278 / 265.
 int token_tiles(const MoeParams &p) {
   const int64_t pairs = (int64_t)p.M * p.k;
   return pairs <= 4 * (int64_t)p.E ? 1 : pairs <= 12 * (int64_t)p.E ? 2 : 4;

@@ -151,17 +151,20 @@ __global__ __launch_bounds__(1024) void k_norm_fwd(NormFwdParams p) {
 // go to `part` once (FP32, added up by k_norm_wgrad in the order of the
 // workgroups, so results do not change from run to run).
 //
-// PARTS: what is given, where that is known here (no test of it in the loop).
+// PARTS: what is given, where that is known here (no test of it in the loop;
+// y without w_post, and dh and y without dz, keep the tests: 48 us at 4096 x 4096
+// with a gate for each channel, against 37 with every part).
 // The next row is then loaded before this one's reduction, for rows of up to
-// 8192 (V <= 2): with dz and dh alone 4096 x 6000 takes 28.5 us, both launches,
-// against 47 with the tests.  Wider rows leave no registers for a second one
+// 8192 (V <= 2): with dz and dh alone 4096 x 6000 takes 35 us against 55 with the
+// tests, with dh alone 26 against 48.  Wider rows leave no registers for a second one
 // and keep the weights in LDS (1548 x 9819, no gate: 63 us against 80 read from
 // L2 again for every row).  Up to 12288 (V = 3) the next row's dz and dh are
 // loaded where this row's are used up, before the reduction, and the rest chunk
 // by chunk as the outputs leave (the same: 58; 1500 x 8320: 36 against 46); with
-// V <= 2 that is slower than the tests alone (4096 x 6000: 52), with V = 4 it
-// spills.  WHOLE: H is a multiple of 8 (no element-by-element ends, which cost
-// registers too).
+// V <= 2 that is slower than the tests alone (4096 x 6000, inputs in the
+// last-level cache: 52 against 47), with V = 4 it spills.  WHOLE: H is a multiple of 8.  Otherwise each load and store has a branch
+// for the row's end, and the kernel spills scalar registers: 1003 x 5125 with a
+// gate for each element takes 30.5 us, 1003 x 5128 18.5.
 enum { GATE_NONE = 0, GATE_ROW = 1, GATE_FULL = 2 };
 // dz, dh, y and w_post; dz and dh; dz, y and w_post; dh alone (the last norm of a network)
 enum { PARTS_ANY = 0, PARTS_ALL = 1, PARTS_NEXT = 2, PARTS_POST = 3, PARTS_LAST = 4 };

@@ -242,7 +242,8 @@ dgf_status dgf_act_bwd_typed(const void *da, const void *g, const void *u, void 
  * ld_gate >= H).  y NULL: the norm before a block alone, h from z = res (no z
  * is written; w_post and gate NULL, alpha 1).  h is taken from z before z is
  * rounded.  rstd [M,2] (r_y, r_z; r = 1 where there is no norm) is optional
- * and is what the backward needs.  z may be res itself (in place).  H is at
+ * and is what the backward needs.  A finite row whose squares add up past FP32's
+ * largest value has r = 0.  z may be res itself (in place).  H is at
  * most 16384 (else DGF_EUNSUPPORTED); eps is positive.  M = 0: DGF_OK, no launch.
  */
 dgf_status dgf_norm_fwd(const void *res, int64_t ld_res, const void *y, int64_t ld_y, const void *w_post,
