@@ -69,6 +69,19 @@ SIGNATURES = {
     "dgf_moe_fwd_workspace": (_SZ, [_I64, _I64, _I64, _I64, _I64, _I64]),
     "dgf_moe_fwd": (_I, [_P, _I64, _P, _I64, _P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _P, _I64, _P, _P,
                          _I64, _I64, _I64, _I64, _I64, _I64, _I64, _I, _P, _SZ, _I, _P]),
+    "dgf_moe_route_workspace": (_SZ, [_I64, _I64, _I64]),
+    "dgf_moe_route": (_I, [_P, _I64, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I, _P, _SZ, _I, _P]),
+    "dgf_moe_route_bwd": (_I, [_P, _P, _I64, _P, _P, _P, _I64, _I64, _I64, _I64, _I, _I, _P]),
+    "dgf_gemm_grouped": (_I, [_I, _P, _I64, _P, _I64, _I64, _P, _I64, _P, _I64, _I64, _P, _I64, _P, _P, _I64, _I64,
+                              _I64, _I64, _I64, _I64, _I, _P]),
+    "dgf_moe_combine": (_I, [_P, _I64, _I64, _P, _P, _P, _I64, _I64, _I64, _I64, _I, _P]),
+    "dgf_moe_combine_bwd": (_I, [_P, _I64, _P, _I64, _I64, _P, _P, _P, _I64, _P, _I64, _I64, _I64, _I, _P]),
+    "dgf_dropout": (_I, [_P, _I64, _P, _I64, _F, ctypes.c_double, _P, _P, _I64, _I64, _I64, _I, _P]),
+    "dgf_pack4": (_I, [_P, _I64, _P, _P, _I64, _I64, _I64, _I, _P]),
+    "dgf_unpack4": (_I, [_P, _P, _P, _I64, _I64, _I64, _I64, _I, _P]),
+    "dgf_gemm_w4": (_I, [_P, _I64, _P, _P, _P, _I64, _I64, _I64, _I64, _I64, _I, _P]),
+    "dgf_ffn_fwd_w4_workspace": (_SZ, [_I64, _I64, _I64]),
+    "dgf_ffn_fwd_w4": (_I, [_P, _I64, _P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _I64, _P, _SZ, _I, _P]),
     "dgf_profile_begin": (_I, [ctypes.POINTER(_P), _I]),
     "dgf_profile_end": (_I, []),
     "dgf_profile_name": (ctypes.c_char_p, [_I]),
@@ -644,6 +657,289 @@ def moe_fwd(x, w_router, w_gate, w_up, w_down, top_k: int, renorm: bool = True, 
                          M, H, I, E, expert_offset, El, top_k, int(renorm), ws.data_ptr(), nbytes, dt,
                          _stream(stream)), "dgf_moe_fwd")
     return (y, ids, probs) if routing else y
+
+
+# ------------------------------------------- mixture of experts over many tokens
+def _flat_of(t, dtype, shape, device: int, name: str):
+    """Pointer of a contiguous tensor of the given type and shape on the device (None: NULL)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if device < 0 or t.get_device() != device:
+        raise ValueError(f"{name}: expected a GPU tensor of the other operands' device")
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor of shape {tuple(shape)}, got {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _here(t: torch.Tensor, name: str) -> int:
+    """The tensor's device, which has to be the one the call launches on."""
+    if not t.is_cuda:
+        raise ValueError(f"{name}: expected a GPU tensor")
+    device = t.get_device()
+    if device != torch.cuda.current_device():
+        raise ValueError(f"{name}: on device {device}, but the call runs on device {torch.cuda.current_device()}")
+    return device
+
+
+class MoePlan(NamedTuple):
+    """Where M tokens go: ids int32 and probs float32 [M, k], offsets int32 [E + 1],
+    rows int32 [M k] (token of each sorted row), pos int32 [M, k] (sorted row of each pair)."""
+
+    ids: torch.Tensor
+    probs: torch.Tensor
+    offsets: torch.Tensor
+    rows: torch.Tensor
+    pos: torch.Tensor
+
+
+_LOGITS = {torch.bfloat16: DGF_BF16, torch.float16: DGF_FP16, torch.float32: DGF_FP32}
+
+
+def _logits(t: torch.Tensor, name: str):
+    """(pointer, leading dimension, dtype code) of a row-major [M, E] matrix of logits."""
+    if t.dtype not in _LOGITS:
+        raise TypeError(f"{name}: expected bfloat16, float16 or float32, got {t.dtype}")
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name}: expected a 2-D row-major view (stride(1) == 1)")
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t.shape[1], _LOGITS[t.dtype]
+
+
+def moe_route(logits, top_k: int, renorm: bool = True, stream=None) -> MoePlan:
+    """Routing of tokens to experts (dgf_moe_route): logits [M, E] (bfloat16, float16
+    or float32), each token to its top_k largest; -inf closes an expert to a token.
+    renorm: weights over the top_k chosen instead of all E."""
+    L = load()
+    lp, ld, dt = _logits(logits, "logits")
+    M, E = logits.shape
+    with _on(stream):
+        _here(logits, "logits")
+        k = max(int(top_k), 0)
+        # one allocation for the int32 outputs: ids, pos, rows, offsets
+        n = M * k
+        ints = logits.new_empty(3 * n + E + 1, dtype=torch.int32)
+        ids, pos, rows, offsets = ints[:n].view(M, k), ints[n:2 * n].view(M, k), ints[2 * n:3 * n], ints[3 * n:]
+        probs = logits.new_empty((M, k), dtype=torch.float32)
+        nbytes = L.dgf_moe_route_workspace(M, E, k)
+        ws = _workspace(nbytes, logits) if nbytes else None
+        _check(L.dgf_moe_route(lp, ld, ids.data_ptr(), probs.data_ptr(), offsets.data_ptr(), rows.data_ptr(),
+                               pos.data_ptr(), M, E, int(top_k), int(renorm), ws.data_ptr() if nbytes else None, nbytes,
+                               dt, _stream(stream)), "dgf_moe_route")
+    return MoePlan(ids, probs, offsets, rows, pos)
+
+
+def moe_route_bwd(dprobs, logits, ids, probs, renorm: bool = True, stream=None):
+    """Gradient of the logits from that of moe_route's probs (dgf_moe_route_bwd), in the logits' type."""
+    L = load()
+    lp, ld, dt = _logits(logits, "logits")
+    M, E = logits.shape
+    k = ids.shape[-1]
+    with _on(stream):
+        device = _here(logits, "logits")
+        dp = _flat_of(dprobs, torch.float32, (M, k), device, "dprobs")
+        ip = _flat_of(ids, torch.int32, (M, k), device, "ids")
+        pp = _flat_of(probs, torch.float32, (M, k), device, "probs")
+        d = logits.new_empty((M, E))
+        _check(L.dgf_moe_route_bwd(dp, lp, ld, ip, pp, d.data_ptr(), E, M, E, k, int(renorm), dt, _stream(stream)),
+               "dgf_moe_route_bwd")
+    return d
+
+
+def gemm_grouped(layout: str, A, B, offsets, rows=None, add=None, out=None, stream=None):
+    """Matrix products grouped by expert (dgf_gemm_grouped).  offsets int32 [E + 1]:
+    expert e has the sorted rows [offsets[e], offsets[e + 1]); rows int32 (optional):
+    sorted row r reads row rows[r] of A (NT, NN) or of B (TN).
+    NT: A [T, K], B [E, N, K] -> [R, N];  NN: A [T, K], B [E, K, N] -> [R, N];
+    TN: A [R, M], B [T, N] -> [E, M, N], the sum over each expert's rows.
+    add=(A2, B2) (NT, NN): a second product in the same sum.  out: where the result
+    goes; rows outside [offsets[0], offsets[E]) are not written."""
+    L = load()
+    if layout not in _LAYOUTS:
+        raise ValueError(f"layout {layout!r}: expected NT, NN or TN")
+    lay, dt = _LAYOUTS[layout], _stored(A)
+    ap, lda = _mat(A, "A")
+    with _on(stream):
+        device = _here(A, "A")
+        E = offsets.numel() - 1
+        op = _flat_of(offsets, torch.int32, (E + 1,), device, "offsets")
+        if lay == DGF_TN:
+            if add is not None:
+                raise ValueError("add: TN takes one pair of operands")
+            (R, M), (T, N) = A.shape, B.shape
+            if rows is None and T != R:
+                raise ValueError(f"B: expected {R} rows, got {T}")
+            bp, ldb = _rows(B, (T, N), A, "B")
+            sb, K, shape = 0, R, (E, M, N)
+        else:
+            T, K = A.shape
+            R = T if rows is None else rows.numel()
+            N = B.shape[1 if lay == DGF_NT else 2]
+            bp, ldb, sb = _experts(B, (E, N, K) if lay == DGF_NT else (E, K, N), A, "B")
+            M, shape = R, (R, N)
+        rp = _flat_of(rows, torch.int32, (R,), device, "rows")
+        a2 = b2 = None
+        lda2 = ldb2 = sb2 = 0
+        if add is not None:
+            a2, lda2 = _rows(add[0], A.shape, A, "add[0]")
+            b2, ldb2, sb2 = _experts(add[1], B.shape, A, "add[1]")
+        if out is None:
+            ld = (N + 7) // 8 * 8
+            out = A.new_empty((*shape[:-1], ld))
+            out = out if ld == N else out[..., :N]
+        sc = 0
+        if lay == DGF_TN:
+            cp, ldc, sc = _experts(out, shape, A, "out")
+        else:
+            cp, ldc = _rows(out, shape, A, "out")
+        _check(L.dgf_gemm_grouped(lay, ap, lda, bp, ldb, sb, a2, lda2, b2, ldb2, sb2, rp, T, op, cp, ldc, sc, M, N, K, E,
+                                  dt, _stream(stream)), "dgf_gemm_grouped")
+    return out
+
+
+def moe_combine(o, pos, probs=None, stream=None):
+    """The experts' outputs o [R, H] back to tokens (dgf_moe_combine): y[m] = sum over
+    j of probs[m, j] o[pos[m, j]], pos int32 [M, k], probs float32 [M, k] (None: 1)."""
+    L = load()
+    dt = _stored(o)
+    op, ldo = _mat(o, "o")
+    R, H = o.shape
+    M, k = pos.shape
+    with _on(stream):
+        device = _here(o, "o")
+        ip = _flat_of(pos, torch.int32, (M, k), device, "pos")
+        pp = _flat_of(probs, torch.float32, (M, k), device, "probs")
+        y = _empty(M, H, o)
+        _check(L.dgf_moe_combine(op, ldo, R, ip, pp, y.data_ptr(), y.stride(0), M, H, k, dt, _stream(stream)),
+               "dgf_moe_combine")
+    return y
+
+
+def moe_combine_bwd(dy, o, pos, probs=None, stream=None):
+    """Gradients of moe_combine (dgf_moe_combine_bwd): d_o [R, H] and dprobs float32
+    [M, k] (None without probs).  Rows of d_o that no pos names are not written."""
+    L = load()
+    dt = _stored(o)
+    op, ldo = _mat(o, "o")
+    R, H = o.shape
+    M, k = pos.shape
+    with _on(stream):
+        device = _here(o, "o")
+        dyp, lddy = _rows(dy, (M, H), o, "dy")
+        ip = _flat_of(pos, torch.int32, (M, k), device, "pos")
+        pp = _flat_of(probs, torch.float32, (M, k), device, "probs")
+        d_o = _empty(R, H, o)
+        dprobs = torch.empty_like(probs) if probs is not None else None
+        _check(L.dgf_moe_combine_bwd(dyp, lddy, op, ldo, R, ip, pp, d_o.data_ptr(), d_o.stride(0),
+                                     dprobs.data_ptr() if probs is not None else None, M, H, k, dt, _stream(stream)),
+               "dgf_moe_combine_bwd")
+    return d_o, dprobs
+
+
+def dropout(x, p: float, rng, res=None, alpha: float = 1.0, out=None, stream=None):
+    """z = alpha res + x keep / (1 - p) (dgf_dropout), the mask from rng, an int64 GPU
+    tensor (seed, step) that the caller advances.  The gradient of x is dropout(dz, p, rng)."""
+    L = load()
+    dt = _stored(x)
+    M, H = x.shape
+    xp, ldx = _mat(x, "x")
+    with _on(stream):
+        device = _here(x, "x")
+        rp, ldr = _rows(res, (M, H), x, "res")
+        gp = _flat_of(rng, torch.int64, (2,), device, "rng")
+        z = out if out is not None else _empty(M, H, x)
+        zp, ldz = _rows(z, (M, H), x, "out") if out is not None else (z.data_ptr(), z.stride(0))
+        _check(L.dgf_dropout(xp, ldx, rp, ldr, alpha, p, gp, zp, ldz, M, H, dt, _stream(stream)), "dgf_dropout")
+    return z
+
+
+# ------------------------------------------------------------------ 4-bit weights
+class Packed4(NamedTuple):
+    """A weight [N, K] in 4 bits, laid out for the few-token products (dgf_pack4):
+    codes uint8 [ceil(N/16), ceil(K/128), 1024], scales [ceil(N/16), ceil(K/128), 16,
+    128 / group] of the type the weight was in."""
+
+    codes: torch.Tensor
+    scales: torch.Tensor
+    shape: tuple
+    group: int
+
+
+def _w4(p: Packed4, dtype, device: int, name: str):
+    """(codes, scales) pointers of a 4-bit weight of the given type."""
+    N, K = p.shape
+    tiles = (-(-N // 16), -(-K // 128))
+    if p.group not in (32, 64, 128):
+        raise ValueError(f"{name}: group {p.group}: 32, 64 or 128 columns share a scale")
+    return (_flat_of(p.codes, torch.uint8, (*tiles, 1024), device, f"{name}: codes"),
+            _flat_of(p.scales, dtype, (*tiles, 16, 128 // p.group), device, f"{name}: scales"))
+
+
+def pack4(w, group: int = 64, stream=None) -> Packed4:
+    """A BF16 or FP16 weight [N, K] in 4 bits, one scale for `group` (32, 64 or 128) columns (dgf_pack4)."""
+    L = load()
+    dt = _stored(w)
+    wp, ldw = _mat(w, "w")
+    N, K = w.shape
+    if group not in (32, 64, 128):
+        raise ValueError(f"group {group}: 32, 64 or 128 columns share a scale")
+    with _on(stream):
+        _here(w, "w")
+        tiles = (-(-N // 16), -(-K // 128))
+        p = Packed4(w.new_empty((*tiles, 1024), dtype=torch.uint8), w.new_empty((*tiles, 16, 128 // group)), (N, K), group)
+        _check(L.dgf_pack4(wp, ldw, p.codes.data_ptr(), p.scales.data_ptr(), N, K, group, dt, _stream(stream)), "dgf_pack4")
+    return p
+
+
+def unpack4(p: Packed4, stream=None) -> torch.Tensor:
+    """Reads a 4-bit weight back in its scales' type, each value rounded once (dgf_unpack4)."""
+    L = load()
+    dt = _stored(p.scales)
+    N, K = p.shape
+    with _on(stream):
+        cp, sp = _w4(p, p.scales.dtype, _here(p.scales, "p"), "p")
+        w = p.scales.new_empty((N, (K + 7) // 8 * 8))
+        _check(L.dgf_unpack4(cp, sp, w.data_ptr(), w.stride(0), N, K, p.group, dt, _stream(stream)), "dgf_unpack4")
+    return w if w.shape[1] == K else w[:, :K]
+
+
+def gemm_w4(x, w4: Packed4, stream=None):
+    """y = x w^T for a few tokens, w [N, K] in 4 bits (dgf_gemm_w4)."""
+    L = load()
+    dt = _stored(x)
+    xp, ldx = _mat(x, "x")
+    M, K = x.shape
+    N = w4.shape[0]
+    if w4.shape[1] != K:
+        raise ValueError(f"w4: expected {K} columns, got {w4.shape[1]}")
+    with _on(stream):
+        cp, sp = _w4(w4, x.dtype, _here(x, "x"), "w4")
+        y = _empty(M, N, x)
+        _check(L.dgf_gemm_w4(xp, ldx, cp, sp, y.data_ptr(), y.stride(0), M, N, K, w4.group, dt, _stream(stream)),
+               "dgf_gemm_w4")
+    return y
+
+
+def ffn_fwd_w4(x, w_gate: Packed4, w_up: Packed4, w_down: Packed4, stream=None):
+    """The FFN for a few tokens with its weights in 4 bits (dgf_ffn_fwd_w4): w_gate,
+    w_up [I, H] and w_down [H, I], all of one group size."""
+    L = load()
+    dt = _stored(x)
+    xp, ldx = _mat(x, "x")
+    M, H = x.shape
+    I = w_gate.shape[0]
+    for name, w, shape in (("w_gate", w_gate, (I, H)), ("w_up", w_up, (I, H)), ("w_down", w_down, (H, I))):
+        if tuple(w.shape) != shape or w.group != w_gate.group:
+            raise ValueError(f"{name}: expected shape {shape} and group {w_gate.group}, got {tuple(w.shape)} and {w.group}")
+    with _on(stream):
+        device = _here(x, "x")
+        ptrs = [q for name, w in (("w_gate", w_gate), ("w_up", w_up), ("w_down", w_down)) for q in _w4(w, x.dtype, device, name)]
+        y = _empty(M, H, x)
+        nbytes = L.dgf_ffn_fwd_w4_workspace(M, H, I)
+        ws = _workspace(nbytes, x)
+        _check(L.dgf_ffn_fwd_w4(xp, ldx, *ptrs, y.data_ptr(), y.stride(0), M, H, I, w_gate.group, ws.data_ptr(), nbytes, dt,
+                                _stream(stream)), "dgf_ffn_fwd_w4")
+    return y
 
 
 class KernelTimer:

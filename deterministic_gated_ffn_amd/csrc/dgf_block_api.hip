@@ -56,15 +56,6 @@ dgf_status check_moe(int64_t M, int64_t H, int64_t I, int64_t E, int64_t e0, int
   return DGF_OK;
 }
 
-// The experts' matrices, `stride` elements apart.
-dgf_status check_experts(const char *name, const void *w, int64_t ld, int64_t stride, int64_t El, int64_t rows,
-                         int64_t cols) {
-  DGF_TRY(check_mat(name, w, ld, rows, cols));
-  if (El > 1 && (stride < (rows - 1) * ld + cols || stride % 8 != 0))
-    return fail(DGF_EINVAL, "%s: expert stride %lld: need a multiple of 8 past the %lld rows", name, (long long)stride, (long long)rows);
-  return DGF_OK;
-}
-
 }  // namespace
 
 extern "C" {

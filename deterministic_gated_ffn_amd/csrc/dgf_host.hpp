@@ -117,6 +117,15 @@ inline dgf_status check_q8(const char *name, const Q8Mat &t, int64_t rows, int64
   return DGF_OK;
 }
 
+// The experts' matrices, `stride` elements apart.
+inline dgf_status check_experts(const char *name, const void *w, int64_t ld, int64_t stride, int64_t El, int64_t rows,
+                         int64_t cols) {
+  DGF_TRY(check_mat(name, w, ld, rows, cols));
+  if (El > 1 && (stride < (rows - 1) * ld + cols || stride % 8 != 0))
+    return fail(DGF_EINVAL, "%s: expert stride %lld: need a multiple of 8 past the %lld rows", name, (long long)stride, (long long)rows);
+  return DGF_OK;
+}
+
 // Public dtype code -> stored type of the kernels: BF16 and FP16 share the
 // tree; an FP32 FFN has no declared leaf rule (its MFMA differs), so it is
 // rejected as unsupported.

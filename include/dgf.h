@@ -68,6 +68,9 @@ typedef enum {
     DGF_EHIP = 4          /* a HIP runtime call or kernel launch failed */
 } dgf_status;
 
+/* Layouts of the matrix products. */
+enum { DGF_NT = 0, DGF_NN = 1, DGF_TN = 2 };
+
 /* Version of this ABI (incremented on any signature change). */
 int dgf_abi_version(void);
 
@@ -342,6 +345,122 @@ dgf_status dgf_moe_fwd(const void *x, int64_t ldx, const void *w_router, int64_t
                        int renorm, void *ws, size_t ws_bytes, int dtype, void *stream);
 
 /*
+ * A mixture of experts over many tokens, forward and backward: the routing of
+ * tokens, products grouped by expert, and the experts' outputs back to tokens.
+ * Each token goes to k experts; its (token, choice) pairs, sorted by expert,
+ * are the R = M k sorted rows.  Limits: 1024 experts, 16 choices, 2^21 tokens,
+ * 2^25 sorted rows.
+ */
+
+/*
+ * Routing.  logits [M,E] (dtype BF16, FP16 or FP32; any ld >= E, aligned to
+ * its elements).  A token takes its k largest logits in descending order, ties
+ * (-0 and +0 are one) to the lowest index; NaN counts as -infinity, +infinity
+ * as FP32's largest value.  An expert whose logit is -infinity is closed to the
+ * token: where fewer than k are open, the choices left over have id -1, weight
+ * 0 and no sorted row (a row of -infinity throughout is a token that goes nowhere).
+ *   probs_j = softmax at the choice over the choices (renorm != 0) or over all E
+ *   offsets [E+1]: expert e has the sorted rows [offsets[e], offsets[e+1]), its
+ *   pairs in the tokens' order; rows [M k]: the token of each sorted row (-1
+ *   behind the last); pos [M,k]: the sorted row of each pair (-1: none).
+ * ids, pos [M,k] int32, probs [M,k] FP32.  M = 0 writes offsets = 0.
+ * Workspace: dgf_moe_route_workspace bytes (0 for a few tokens).
+ *
+ * The backward gives dlogits [M,E] (the logits' type) from dprobs: with s the sum
+ * over the choices of dprobs probs, dlogits_e = P_e (dprobs_e - s), P the softmax
+ * (renorm: probs at the choices and 0 elsewhere, logits are not read and may be NULL).
+ */
+size_t dgf_moe_route_workspace(int64_t M, int64_t E, int64_t k);
+dgf_status dgf_moe_route(const void *logits, int64_t ld, int32_t *ids, float *probs, int32_t *offsets, int32_t *rows,
+                         int32_t *pos, int64_t M, int64_t E, int64_t k, int renorm, void *ws, size_t ws_bytes, int dtype,
+                         void *stream);
+dgf_status dgf_moe_route_bwd(const float *dprobs, const void *logits, int64_t ld, const int32_t *ids, const float *probs,
+                             void *dlogits, int64_t ld_d, int64_t M, int64_t E, int64_t k, int renorm, int dtype,
+                             void *stream);
+
+/*
+ * Products grouped by expert.  offsets [E+1] (int32, on the device, ascending):
+ * expert e has the rows [offsets[e], offsets[e+1]) of the sorted ones; a range of
+ * experts is its part of the offsets with its matrices.  rows (int32, optional):
+ * sorted row r reads row rows[r] of a matrix of T rows, else row r.
+ *   DGF_NT: C[r] = A[rows[r]] B_e^T      A [T,K] (no rows: [M,K]), B [E,N,K], C [M,N]
+ *   DGF_NN: C[r] = A[rows[r]] B_e        A [T,K], B [E,K,N], C [M,N]
+ *   DGF_TN: C_e = sum over e's rows r of A[r]^T B[rows[r]]
+ *                                        A [K,M], B [T,N] (no rows: [K,N]), C [E,M,N]
+ * so M (NT, NN) or K (TN) is the number of sorted rows.  A2, B2 (NT, NN; both or
+ * neither; shaped as A and B) add A2[rows[r]] B2_e to the same sum.  The experts'
+ * matrices have a leading dimension and a stride from one to the next.
+ * Sums are FP32 over ascending K in one order whatever the other rows are; each
+ * output is rounded once.  Rows of C outside [offsets[0], offsets[E]) are left as
+ * they were; K = 0 and experts without rows (TN) give +0.  Offsets are taken
+ * within [0, rows]; an index outside [0, T) reads as a row of zeros.
+ */
+dgf_status dgf_gemm_grouped(int layout, const void *A, int64_t lda, const void *B, int64_t ldb, int64_t stride_b,
+                            const void *A2, int64_t lda2, const void *B2, int64_t ldb2, int64_t stride_b2,
+                            const int32_t *rows, int64_t T, const int32_t *offsets, void *C, int64_t ldc,
+                            int64_t stride_c, int64_t M, int64_t N, int64_t K, int64_t E, int dtype, void *stream);
+
+/*
+ * The experts' outputs o [R,H] (sorted rows) back to tokens:
+ *   y[m] = sum over j of probs[m,j] o[pos[m,j]]        (probs NULL: 1)
+ * in FP32, j ascending; choices with pos outside [0, R) add nothing.  Backward:
+ *   d_o[pos[m,j]] = probs[m,j] dy[m],  dprobs[m,j] = <dy[m], o[pos[m,j]]>  (0 without a row)
+ * dprobs may be NULL (o is not read then).  A row of d_o that no pos names is
+ * left as it was; no two pos may name the same row.
+ */
+dgf_status dgf_moe_combine(const void *o, int64_t ld_o, int64_t R, const int32_t *pos, const float *probs, void *y,
+                           int64_t ldy, int64_t M, int64_t H, int64_t k, int dtype, void *stream);
+dgf_status dgf_moe_combine_bwd(const void *dy, int64_t lddy, const void *o, int64_t ld_o, int64_t R, const int32_t *pos,
+                               const float *probs, void *d_o, int64_t ld_do, float *dprobs, int64_t M, int64_t H,
+                               int64_t k, int dtype, void *stream);
+
+/*
+ * Dropout with the residual: z = alpha res + keep x / (1 - p), res optional
+ * (alpha is not used then).  The mask is never stored: rng (device memory) holds {seed,
+ * step}, and the eight values of columns [8 c, 8 c + 8) of row m are kept where
+ * the 16-bit halves (low first) of Philox-4x32-10 with counter {m ceil(H/8) + c,
+ * step} and key seed, each 64 bits, low words first, are not below round(65536 p);
+ * p here is that integer over 65536.  The gradient of x is this call on dz with
+ * the same rng.  A graph's replays draw new masks when it also advances step.
+ * z may be x or res itself.  0 <= p < 1 - 2^-17.
+ */
+dgf_status dgf_dropout(const void *x, int64_t ldx, const void *res, int64_t ld_res, float alpha, double p,
+                       const int64_t *rng, void *z, int64_t ldz, int64_t M, int64_t H, int dtype, void *stream);
+
+/*
+ * Weights in 4 bits.  A row's columns are cut into groups of 32, 64 or 128 (the
+ * last may be short); a group with largest magnitude A keeps the scale s = A/7
+ * rounded to the stored type, and one code a value, c = rint(w/s) within [-7, 7]:
+ * it reads back as s c.  (Where 7 s would round to infinity, s is the next value
+ * below.)  s = 0 reads back as 0 throughout; a group that holds an
+ * infinity or a NaN keeps s = NaN.  Layout, for tiles of 16 rows x 128 columns,
+ * ceil(N/16) x ceil(K/128) of them, the columns' fastest: codes, 1024 bytes a
+ * tile, 16-byte aligned: dword 4 l + i of tile lane l holds row l % 16, columns
+ * 32 i + 8 (l / 16) + 0..7, column 2 d in bits 4 d.. and 2 d + 1 in bits 16 + 4 d..,
+ * as c + 8; scales, 16 x 128/group a tile, row-major, stored type, 8-byte aligned.
+ * Rows and columns past N and K are codes of 0.
+ */
+dgf_status dgf_pack4(const void *w, int64_t ldw, void *codes, void *scales, int64_t N, int64_t K, int64_t group, int dtype,
+                     void *stream);
+dgf_status dgf_unpack4(const void *codes, const void *scales, void *w, int64_t ldw, int64_t N, int64_t K, int64_t group,
+                       int dtype, void *stream);
+
+/*
+ * y [M,N] = x [M,K] w^T with w in 4 bits, and the FFN y = W_down (silu(W_gate x)
+ * (W_up x)) with all three.  Made for a few tokens: the weights are read once for
+ * every 32.  Sums are FP32 in an order that does not depend on M; y is rounded
+ * once; the activation passes between the FFN's two kernels to 2^-16 of its value.
+ * Inputs are finite.  M <= 65536.  Workspace: dgf_ffn_fwd_w4_workspace bytes.
+ */
+dgf_status dgf_gemm_w4(const void *x, int64_t ldx, const void *codes, const void *scales, void *y, int64_t ldy, int64_t M,
+                       int64_t N, int64_t K, int64_t group, int dtype, void *stream);
+size_t dgf_ffn_fwd_w4_workspace(int64_t M, int64_t H, int64_t I);
+dgf_status dgf_ffn_fwd_w4(const void *x, int64_t ldx, const void *gate_codes, const void *gate_scales,
+                          const void *up_codes, const void *up_scales, const void *down_codes, const void *down_scales,
+                          void *y, int64_t ldy, int64_t M, int64_t H, int64_t I, int64_t group, void *ws, size_t ws_bytes,
+                          int dtype, void *stream);
+
+/*
  * Diagnostic entry points (stage isolation and shard emulation; the FFN
  * entry points above are composed of the same kernels).
  *
@@ -353,7 +472,6 @@ dgf_status dgf_moe_fwd(const void *x, int64_t ldx, const void *w_router, int64_t
  * (0 when none is needed, e.g. DGF_TN with K <= 64, which reads A and B in
  * place; a NULL ws is then accepted).
  */
-enum { DGF_NT = 0, DGF_NN = 1, DGF_TN = 2 };
 size_t dgf_gemm_tree_workspace(int layout, int64_t M, int64_t N, int64_t K);
 dgf_status dgf_gemm_tree(int layout, const void *A, int64_t lda, const void *B, int64_t ldb,
                          void *C, int64_t ldc, int64_t M, int64_t N, int64_t K,
