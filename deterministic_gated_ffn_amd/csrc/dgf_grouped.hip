@@ -5,8 +5,7 @@
 namespace dgf {
 namespace {
 
-constexpr int kBK = 64;          // contraction elements of a stage
-constexpr int kGroupedWaves = 8;  // 2 over the tile's rows x 4 over its columns
+constexpr int kU = 32;  // contraction elements of a stage
 
 typedef __attribute__((address_space(3))) uint16_t lds_u16;
 typedef short s16x4 __attribute__((ext_vector_type(4)));
@@ -17,13 +16,18 @@ __device__ const uint4 kZeros[1] = {};
 // uniform), lane l's at dst + 16 l, without passing through registers.  The
 // compiler does not count the load: stage_wait() below does.
 __device__ __forceinline__ void lds_load(const char *src, uint32_t dst) {
-  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "s"(dst) : "memory");
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "s"(__builtin_amdgcn_readfirstlane(dst))
+               : "memory");
 }
-__device__ __forceinline__ void stage_wait() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+// All but the N youngest of this wave's loads have landed; then every wave's.
+template <int N>
+__device__ __forceinline__ void stage_wait() {
+  asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(N) : "memory");
+}
 
-// Where 16 bytes of an operand's tile of BX rows (or columns) x kBK go in LDS.
-//  - contraction contiguous (TR false): row r takes 128 bytes, its 16-byte piece
-//    c sits at c ^ (r & 7): the 16 rows of a fragment read take all banks.
+// Where 16 bytes of an operand's tile of BX rows (or columns) x kU go in LDS.
+//  - contraction contiguous (TR false): row r takes 64 bytes, its 16-byte piece
+//    c sits at c ^ (r / 2 & 3): the rows of a fragment read take all banks.
 //  - contraction across rows (TR): row k takes 2 BX bytes and is read in
 //    transposed blocks of 4 k x 16 columns (32 bytes of 4 rows each), whose
 //    rows sw(k) moves to different banks.
@@ -33,44 +37,35 @@ __device__ __forceinline__ int tr_swizzle(int k) {
   return BX >= 128 ? s << 1 : (s & 3) << 1;
 }
 
-// One operand's loader: the thread's pieces of a stage and their addresses.
-template <bool TR, int BX>
-struct Loader {
-  static constexpr int NL = BX / 64;  // wave loads of 1 KB a stage and wave
-  static constexpr int kPieces = BX / 8;  // 16-byte pieces of a k row (TR)
-  const char *p[NL];
-  uint32_t step[NL];  // bytes to the next stage; 0 where the piece is none of the tile's
-  int koff[NL];       // TR: k row of the piece; else: first k of the piece
-
-  // TR false: row i of the tile at base(i) (null: none)
-  template <class F>
-  __device__ __forceinline__ void start_rows(int wave, int lane, F &&base) {
-#pragma unroll
-    for (int i = 0; i < NL; ++i) {
-      const int row = 8 * (wave + kGroupedWaves * i) + (lane >> 3);
-      const char *b = base(row);
-      koff[i] = 8 * ((lane & 7) ^ (lane >> 3));
-      p[i] = b ? b + 2 * koff[i] : reinterpret_cast<const char *>(kZeros);
-      step[i] = b ? 2 * kBK : 0;
-    }
-  }
-  // TR: k row k, columns c.. of the tile
-  static __device__ __forceinline__ int k_row(int wave, int lane, int i) {
-    return (wave + kGroupedWaves * i) * (64 / kPieces) + lane / kPieces;
-  }
-  static __device__ __forceinline__ int col(int lane, int k) { return 8 * ((lane % kPieces) ^ tr_swizzle<BX>(k)); }
+// A wave's pieces of a stage: 1 KB loads `wave`, `wave + waves`, ... of the BX / 8
+// that the operand's tile takes; 16 bytes a lane.
+template <bool TR, int BX, int WAVES>
+struct Pieces {
+  // (a wave past the last load repeats another's: every wave counts the same loads)
+  static constexpr int kAll = BX / 16, NL = (kAll + WAVES - 1) / WAVES;
+  static __device__ __forceinline__ int load(int wave, int i) { return kAll % WAVES ? (wave + WAVES * i) % kAll : wave + WAVES * i; }
+  static constexpr int kRow = BX / 8;  // pieces of a k row (TR)
+  // TR false: row of the tile and first k of the lane's piece
+  static __device__ __forceinline__ int row(int wave, int lane, int i) { return 16 * load(wave, i) + (lane >> 2); }
+  static __device__ __forceinline__ int k_of(int lane) { return 8 * ((lane & 3) ^ (lane >> 3 & 3)); }
+  // TR: its k row and first column
+  static __device__ __forceinline__ int k_row(int wave, int lane, int i) { return load(wave, i) * (64 / kRow) + lane / kRow; }
+  // (the next load's k row is kMore further, at the same column: the swizzle repeats after 16)
+  static constexpr int kMore = WAVES * (64 / kRow);
+  static_assert(!TR || NL == 1 || (kAll % WAVES == 0 && kMore % 16 == 0), "one address for all of a wave's loads");
+  static __device__ __forceinline__ int col(int lane, int k) { return 8 * ((lane % kRow) ^ tr_swizzle<BX>(k)); }
 };
 
 template <class T, bool TR, int BX>
-__device__ __forceinline__ typename T::frag frag_at(const uint16_t *tile, int x0, int kk, int lane) {
+__device__ __forceinline__ typename T::frag frag_at(const uint16_t *tile, int x0, int lane) {
   const int i = lane & 15, g = lane >> 4;
   if constexpr (!TR) {
-    return *reinterpret_cast<const typename T::frag *>(tile + (x0 + i) * kBK + 8 * ((4 * kk + g) ^ (i & 7)));
+    return *reinterpret_cast<const typename T::frag *>(tile + (x0 + i) * kU + 8 * (g ^ (i >> 1 & 3)));
   } else {
     union { s16x4 h[2]; typename T::frag f; } u;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int k = 32 * kk + 8 * g + 4 * h + (i >> 2);
+      const int k = 8 * g + 4 * h + (i >> 2);
       const int piece = ((x0 >> 3) + ((i & 3) >> 1)) ^ tr_swizzle<BX>(k);
       const uint16_t *a = tile + k * BX + 8 * piece + 4 * (i & 1);
       u.h[h] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4 *)(a));
@@ -79,280 +74,520 @@ __device__ __forceinline__ typename T::frag frag_at(const uint16_t *tile, int x0
   }
 }
 
-// Zeros from contraction element kv on, in a stage of rows x kBK (TR false).
-__device__ __forceinline__ void zero_tail(uint16_t *tile, int rows, int kv) {
-  const int c0 = kv >> 3;  // the piece that ends the row; those behind it were loaded as zeros
-  if (kv & 7)
-    for (int r = threadIdx.x; r < rows; r += 64 * kGroupedWaves) {
-      uint16_t *q = tile + r * kBK + 8 * (c0 ^ (r & 7));
-      for (int e = kv & 7; e < 8; ++e) q[e] = 0;
-    }
+// The lane number, as a value the compiler does not carry addresses made of it along
+// for (they would take the registers of the accumulators).
+__device__ __forceinline__ int fresh(int lane) {
+  asm volatile("" : "+v"(lane));
+  return lane;
 }
 
-// One tile of 32 FM rows x 64 FN columns at (row0, n0) of expert e, whose rows
-// (TN: contraction) are [lo, hi).
-template <class T, int LAYOUT, int FM, int FN>
-__device__ __forceinline__ void tile(const GroupedParams &p, char *lds, int e, int64_t lo, int64_t hi, int64_t row0, int n0) {
-  constexpr bool ATR = LAYOUT == DGF_LAYOUT_TN, BTR = LAYOUT != DGF_LAYOUT_NT;
-  constexpr int BM = 32 * FM, BN = 64 * FN, kStage = (BM + BN) * kBK * 2;
-  typedef Loader<ATR, BM> LA;
-  typedef Loader<BTR, BN> LB;
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = wave >> 2, wn = wave & 3;
-  const int64_t klen = ATR ? hi - lo : p.K;
-  const int nb = (int)((klen + kBK - 1) / kBK), total = nb * p.terms;
-  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)lds;
-
-  LA la;
-  LB lb;
-  int idx[LB::NL];  // TN with a row list: the rows of the stage to load next
-  auto open = [&](int term) {
-    const GroupedTerm &t = p.t[term];
-    if constexpr (!ATR) {
-      la.start_rows(wave, lane, [&](int row) -> const char * {
-        const int64_t r = row0 + row;
-        if (r >= hi) return nullptr;
-        const int64_t a = p.rows ? p.rows[r] : r;
-        if (a < 0 || a >= p.T) return nullptr;
-        return reinterpret_cast<const char *>(t.A + a * t.lda);
-      });
-    } else {
-#pragma unroll
-      for (int i = 0; i < LA::NL; ++i) {
-        const int k = LA::k_row(wave, lane, i);
-        const int64_t c = row0 + LA::col(lane, k);
-        la.koff[i] = c < p.M ? k : 1 << 30;
-        la.p[i] = reinterpret_cast<const char *>(t.A + (lo + k) * t.lda + c);
-      }
-    }
-    if constexpr (!BTR) {
-      lb.start_rows(wave, lane, [&](int row) -> const char * {
-        return n0 + row < p.N ? reinterpret_cast<const char *>(t.B + e * t.stride_b + (int64_t)(n0 + row) * t.ldb) : nullptr;
-      });
-    } else {
-#pragma unroll
-      for (int i = 0; i < LB::NL; ++i) {
-        const int k = LB::k_row(wave, lane, i);
-        const int c = n0 + LB::col(lane, k);
-        lb.koff[i] = c < p.N ? k : 1 << 30;
-        if (!ATR) lb.p[i] = reinterpret_cast<const char *>(t.B + e * t.stride_b + (int64_t)k * t.ldb + c);
-        else if (!p.rows) lb.p[i] = reinterpret_cast<const char *>(t.B + (lo + k) * t.ldb + c);
-        else lb.p[i] = reinterpret_cast<const char *>(t.B + c);
-      }
-    }
-  };
-  // the row list's entries for the stage that starts at k0
-  auto list = [&](int64_t k0) {
-    if constexpr (ATR) {
-      if (p.rows)
-#pragma unroll
-        for (int i = 0; i < LB::NL; ++i) {
-          const int64_t k = k0 + LB::k_row(wave, lane, i);
-          idx[i] = k < klen ? p.rows[lo + k] : -1;
-        }
-    }
-  };
-  const char *const zeros = reinterpret_cast<const char *>(kZeros);
-  auto load = [&](int j) {
-    const int term = j >= nb;
-    const int64_t k0 = (int64_t)(j - term * nb) * kBK;
-    const bool tail = k0 + kBK > klen;
-    const uint32_t dst = lds0 + (j & 1) * kStage + wave * 1024;
-    const int64_t a_step = p.t[term].lda * (2 * kBK), b_step = p.t[term].ldb * (2 * kBK);
-#pragma unroll
-    for (int i = 0; i < LA::NL; ++i) {
-      const char *q = la.p[i];
-      if constexpr (ATR) {
-        if (la.koff[i] >= klen - k0) q = zeros;
-        la.p[i] += a_step;
-      } else {
-        if (tail && k0 + la.koff[i] >= klen) q = zeros;
-        la.p[i] += la.step[i];
-      }
-      lds_load(q, dst + i * 1024 * kGroupedWaves);
-    }
-#pragma unroll
-    for (int i = 0; i < LB::NL; ++i) {
-      const char *q = lb.p[i];
-      if constexpr (!BTR) {
-        if (tail && k0 + lb.koff[i] >= klen) q = zeros;
-        lb.p[i] += lb.step[i];
-      } else if (ATR && p.rows) {
-        q = (uint32_t)idx[i] < (uint32_t)p.T && lb.koff[i] < (1 << 30) ? q + (int64_t)idx[i] * p.t[0].ldb * 2 : zeros;
-      } else {
-        if (lb.koff[i] >= klen - k0) q = zeros;
-        lb.p[i] += b_step;
-      }
-      lds_load(q, dst + BM * kBK * 2 + i * 1024 * kGroupedWaves);
-    }
-    if (j + 1 == nb && p.terms == 2) open(1);
-    list(k0 + kBK);
-  };
-
-  f32x4 acc[FM][FN];
-#pragma unroll
-  for (int m = 0; m < FM; ++m)
-#pragma unroll
-    for (int n = 0; n < FN; ++n) acc[m][n] = f32x4{0.f, 0.f, 0.f, 0.f};
-
-  if (total > 0) {
-    open(0);
-    list(0);
-    load(0);
-  }
-  for (int j = 0; j < total; ++j) {
-    stage_wait();  // stage j has landed in every wave; stage j - 1 is read out
-    uint16_t *sa = reinterpret_cast<uint16_t *>(lds + (j & 1) * kStage), *sb = sa + BM * kBK;
-    if (j + 1 < total) load(j + 1);
-    if ((j + 1 == nb || j + 1 == total) && (klen & 7) && !(ATR && BTR)) {
-      const int kv = (int)(klen - (int64_t)(nb - 1) * kBK);
-      if (!ATR) zero_tail(sa, BM, kv);
-      if (!BTR) zero_tail(sb, BN, kv);
-      asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    }
-#pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
-      typename T::frag a[FM], b[FN];
-#pragma unroll
-      for (int n = 0; n < FN; ++n) b[n] = frag_at<T, BTR, BN>(sb, (wn * FN + n) * 16, kk, lane);
-#pragma unroll
-      for (int m = 0; m < FM; ++m) a[m] = frag_at<T, ATR, BM>(sa, (wm * FM + m) * 16, kk, lane);
-#pragma unroll
-      for (int m = 0; m < FM; ++m)
-#pragma unroll
-        for (int n = 0; n < FN; ++n) acc[m][n] = T::mfma(b[n], a[m], acc[m][n]);
-    }
-  }
-
-  // lane l holds columns 4 (l / 16) .. + 3 of row l % 16 of each 16 x 16 block
-  const int i = lane & 15, g = lane >> 4;
-  const int64_t rend = ATR ? p.M : hi;
-  uint16_t *C = ATR ? p.C + e * p.stride_c : p.C;
-#pragma unroll
-  for (int m = 0; m < FM; ++m) {
-    const int64_t r = row0 + (wm * FM + m) * 16 + i;
-    if (r >= rend) continue;
-#pragma unroll
-    for (int n = 0; n < FN; ++n) {
-      const int c = n0 + (wn * FN + n) * 16 + 4 * g;
-      uint16_t *o = C + r * p.ldc + c;
-      const uint2 v = make_uint2(T::pack(acc[m][n][0], acc[m][n][1]), T::pack(acc[m][n][2], acc[m][n][3]));
-      if (c + 4 <= p.N) {
-        *reinterpret_cast<uint2 *>(o) = v;
-      } else {
-        const uint32_t w[2] = {v.x, v.y};
-        for (int q = 0; c + q < p.N && q < 4; ++q) o[q] = (uint16_t)(w[q >> 1] >> (16 * (q & 1)));
-      }
-    }
+// Zeros behind contraction element kv of a stage's rows (TR false), in the piece that
+// holds it: those behind that piece were loaded as zeros.
+template <int THREADS>
+__device__ __forceinline__ void zero_tail(uint16_t *tile, int rows, int kv) {
+  for (int r = fresh(threadIdx.x); r < rows; r += THREADS) {
+    uint16_t *q = tile + r * kU + 8 * ((kv >> 3) ^ (r >> 1 & 3));
+    for (int e = kv & 7; e < 8; ++e) q[e] = 0;
   }
 }
 
 // The rows [lo, hi) of expert e, within the R there are whatever the offsets hold.
-__device__ __forceinline__ void expert_rows(const GroupedParams &p, int e, int64_t &lo, int64_t &hi) {
-  lo = p.off[e];
-  hi = p.off[e + 1];
-  lo = lo < 0 ? 0 : lo > p.R ? p.R : lo;
-  hi = hi < lo ? lo : hi > p.R ? p.R : hi;
+// (Read as constants: by the scalar unit, beside the counted vector loads.)
+__device__ __forceinline__ void expert_rows(const GroupedParams &p, int e, int &lo, int &hi) {
+  const auto *off = (const __attribute__((address_space(4))) int *)(uintptr_t)p.off;
+  const int R = (int)p.R, l = off[e], h = off[e + 1];
+  lo = l < 0 ? 0 : l > R ? R : l;
+  hi = h < lo ? lo : h > R ? R : h;
 }
 
-// NT, NN: finds the tile's expert by the prefix sum of the experts' row tiles.
-template <class T, int LAYOUT, int FM, int FN>
-__global__ __launch_bounds__(64 * kGroupedWaves) void k_grouped_rows(GroupedParams p) {
-  extern __shared__ __attribute__((aligned(16))) char lds[];
-  constexpr int BM = 32 * FM;
-  const int lane = threadIdx.x & 63;
-  int t = xcd_tile(blockIdx.x, p.tiles);
-  int found = -1, local = 0, mt = 0;
-  int64_t lo = 0, hi = 0;
-  for (int e0 = 0; e0 < p.E && found < 0; e0 += 64) {
-    int64_t l = 0, h = 0;
-    if (e0 + lane < p.E) expert_rows(p, e0 + lane, l, h);
-    const int m = (int)((h - l + BM - 1) / BM);
-    int sum = m * p.tiles_n;
-    const int own = sum;
+template <class V>
+__device__ __forceinline__ V uniform(V v) {
+  static_assert(sizeof(V) == 4, "one register");
+  return __builtin_bit_cast(V, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, v)));
+}
+__device__ __forceinline__ int64_t uniform64(int64_t v) {
+  return (int64_t)(uint32_t)uniform((int)v) | (int64_t)uniform((int)(v >> 32)) << 32;
+}
+
+// One output tile of expert e: columns [n0, n0 + 64 w) and, NT and NN, the sorted rows
+// [lo, hi); TN: rows of C from row0, summed over the sorted rows [lo, hi).
+struct Tile {
+  int e, lo, hi, row0, n0, w;
+};
+constexpr int kNoTile = -1;  // its e: there is none
+
+// A workgroup's tiles.  Each expert's output is cut into tiles (NT, NN: of up to BM rows,
+// as even as they come in units of 64; BN columns), those of up to 8 row tiles for a column
+// tile in turn.  Each XCD takes a run of all tiles, equal by what they cost, and deals it
+// out to its workgroups in turn: those that share rows or weights run at one time.  What is
+// left for less than half of a last round is cut into tiles of fewer columns, one for each
+// workgroup.
+//   cost of a tile: NT, NN: its height h in units of 64 rows, and 1 (the products, and the
+//   weights' columns that it reads); TN: its stages, and kTileCost (its own store)
+// The tiles of a run are looked up 32 at a time, one a lane, and kept in LDS: their numbers
+// by expert, summed up (every wave writes the same values), and the next 64 of them.
+constexpr int kTileCost = 8;
+
+template <int LAYOUT, int BM, int BN>
+struct Tiles {
+  static constexpr bool TN = LAYOUT == DGF_LAYOUT_TN;
+  static constexpr int HM = BM / 64, CW = BN / 64;
+  const GroupedParams &p;
+  int *next;   // LDS: 64 tiles of 4 values
+  int *sums;   // LDS: [E + 1] tiles of the experts before
+  int first, count, place, step;  // the XCD's run; this workgroup's place among the `step` that share it
+
+  static constexpr int bytes(int E) { return 64 * 16 + (E + 4) / 4 * 16; }
+
+  __device__ __forceinline__ int tiles_of(int rows) const {
+    return (TN ? p.tiles_m : ((rows + 63) / 64 + HM - 1) / HM) * p.tiles_n;
+  }
+  __device__ __forceinline__ int64_t cost_of(int rows) const {
+    if (TN) return ((int64_t)(rows + 2 * kU - 1) / (2 * kU) * 2 + kTileCost) * p.tiles_m * p.tiles_n;
+    const int u = (rows + 63) / 64;
+    return (int64_t)(u + (u + HM - 1) / HM) * p.tiles_n;
+  }
+  template <class V>
+  static __device__ __forceinline__ V wave_scan(V v, int lane) {
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
-      const int v = __shfl_up(sum, d);
-      if (lane >= d) sum += v;
+      const V o = __shfl_up(v, d);
+      if (lane >= d) v += o;
     }
-    const uint64_t past = __ballot(sum > t);
-    if (past) {
-      const int w = __builtin_ctzll(past);
-      found = e0 + w;
-      local = t - (__shfl(sum, w) - __shfl(own, w));
-      mt = __shfl(m, w);
-      lo = __shfl((int)l, w);
-      hi = __shfl((int)h, w);
-    } else {
-      t -= __shfl(sum, 63);
+    return v;
+  }
+  // The first tile that begins at cost `from` or later, e's costs starting at `before`.
+  __device__ __forceinline__ void start(int b, int n, int lane) {
+    int64_t all = 0;
+    int tiles = 0;
+    if (lane == 0) sums[0] = 0;
+    for (int e0 = 0; e0 < p.E; e0 += 64) {
+      int l = 0, h = 0;
+      if (e0 + lane < p.E) expert_rows(p, e0 + lane, l, h);
+      const bool in = e0 + lane < p.E;
+      all += __shfl(wave_scan(in ? cost_of(h - l) : 0, lane), 63);
+      const int t = wave_scan(in ? tiles_of(h - l) : 0, lane) + tiles;
+      if (in) sums[e0 + lane + 1] = t;
+      tiles = __shfl(t, 63);
+    }
+    all = uniform64(all);
+    const int xcd = b & 7;
+    const int64_t from = uniform64(all * xcd / 8), to = uniform64(all * (xcd + 1) / 8);
+    int begin = tiles, end = tiles;
+    bool open = true;
+    int64_t base = 0;
+    for (int e0 = 0; e0 < p.E; e0 += 64) {
+      int l = 0, h = 0;
+      if (e0 + lane < p.E) expert_rows(p, e0 + lane, l, h);
+      const int64_t cost = e0 + lane < p.E ? cost_of(h - l) : 0, sum = wave_scan(cost, lane) + base;
+      const uint64_t a = __ballot(sum > from), z = __ballot(sum > to);
+      const int t = tiles_of(h - l);
+      if (open && a) {
+        const int x = __builtin_ctzll(a);
+        const int64_t c = __shfl(cost, x);
+        begin = sums[e0 + x] + (int)(((from - (__shfl(sum, x) - c)) * __shfl(t, x) + c - 1) / c);
+        open = false;
+      }
+      if (z) {
+        const int x = __builtin_ctzll(z);
+        const int64_t c = __shfl(cost, x);
+        end = sums[e0 + x] + (int)(((to - (__shfl(sum, x) - c)) * __shfl(t, x) + c - 1) / c);
+        break;
+      }
+      base = __shfl(sum, 63);
+    }
+    first = uniform(begin);
+    count = uniform(end - begin);
+    place = b >> 3;
+    step = n >> 3;
+  }
+  // Tiles i0 .. i0 + 31 of this workgroup, into their half of `next`.
+  __device__ __forceinline__ void fill(int i0, int lane) const {
+    if (lane >= 32) return;
+    const int i = i0 + lane, rounds = count / step, rest = count % step;
+    // parts of a tile of the last round
+    const int split = CW >= 4 && rest * 4 <= step ? 4 : CW >= 2 && rest * 2 <= step ? 2 : 1;
+    int at = i * step + place, part = -1;
+    if (i >= rounds) {
+      at = rounds * step + place / split;
+      part = place % split;
+    }
+    int4 v = make_int4(kNoTile, 0, 0, 0);
+    if (i < rounds || (i == rounds && place < rest * split)) {
+      at += first;
+      int e = 0, past = p.E;  // the last expert whose tiles start at or before it
+      while (past - e > 1) {
+        const int mid = (e + past) / 2;
+        if (sums[mid] <= at) e = mid;
+        else past = mid;
+      }
+      int lo, hi;
+      expert_rows(p, e, lo, hi);
+      const int units = (hi - lo + 63) / 64, rows = TN ? p.tiles_m : (units + HM - 1) / HM;
+      const int c = at - sums[e];
+      // (offsets that are not ascending can make the sums wrap: no tile then)
+      if ((uint32_t)c < (uint32_t)tiles_of(hi - lo)) {
+        const int group = c / (8 * p.tiles_n) * 8, of = rows - group < 8 ? rows - group : 8, in = c - group * p.tiles_n;
+        const int column = in / of, row = group + in % of;
+        const int w = part < 0 ? CW : CW / split;
+        part = part < 0 ? 0 : part;
+        if constexpr (!TN) {
+          const int even = units / rows, more = units % rows, h = 64 * (even + (row < more));
+          lo += 64 * (row * even + (row < more ? row : more));
+          hi = hi - lo < h ? hi : lo + h;
+        }
+        // a part behind the last column is of width 0: nothing to do
+        v = make_int4(e | (column * BN + part * w * 64 < p.N ? w : 0) << 10 | part << 13 | column << 15, lo, hi, row);
+      }
+    }
+    reinterpret_cast<int4 *>(next)[i & 63] = v;
+  }
+  __device__ __forceinline__ Tile get(int i) const {
+    const int4 v = reinterpret_cast<const int4 *>(next)[i & 63];
+    const int x = uniform(v.x), w = x >> 10 & 7;
+    return Tile{x < 0 ? kNoTile : x & 1023, uniform(v.y), uniform(v.z), TN ? uniform(v.w) * BM : 0, (x >> 15) * BN + (x >> 13 & 3) * w * 64, w};
+  }
+};
+
+// A workgroup's tiles as one stream of stages: while a stage is multiplied, the loads of
+// the next ones, of this tile or the ones after it, are under way.
+template <class T, int LAYOUT, int WN, int FMAX, int FNMAX, int NS>
+struct Stream {
+  static constexpr bool ATR = LAYOUT == DGF_LAYOUT_TN, BTR = LAYOUT != DGF_LAYOUT_NT;
+  static constexpr int WAVES = 2 * WN, BM = 32 * FMAX, BN = 16 * WN * FNMAX, kStage = (BM + BN) * kU * 2;
+  static constexpr int kNone = 1 << 30;
+  static_assert(NS % 2 == 0, "stages come in pairs");
+  typedef Pieces<ATR, BM, WAVES> PA;
+  typedef Pieces<BTR, BN, WAVES> PB;
+  static constexpr int kLoads = PA::NL + PB::NL;
+  static constexpr int kPerRow = 64 / PB::kRow;  // k rows of a 1 KB load (TR)
+
+  const GroupedParams &p;
+  char *lds;
+  int lane, wave, wm, wn;
+  uint32_t lds0;
+  // the loader: its tile, what is left of it and the addresses of the next stage's pieces
+  Tiles<LAYOUT, BM, BN> tiles;
+  int ahead, next_number;  // its number in the run (kNoTile: no more), and the one to look at next
+  int end;         // TN: its last sorted row, and 1
+  int left, term;  // contraction elements left of the term
+  int slot;        // place of the next stage to load
+  // (TR: of the first, the others a fixed number of k rows further)
+  static constexpr int NA = ATR ? 1 : PA::NL, NB = BTR ? 1 : PB::NL;
+  const char *pa[NA], *pb[NB];
+  int ka[NA], kb[NB];  // first k of the piece (kNone: zeros)
+  int idx[PB::NL * kPerRow];  // TN with a row list: the next stage's rows
+  int at;          // place of the next stage to enter
+
+  __device__ __forceinline__ Stream(const GroupedParams &p_, char *lds_)
+      : p(p_), lds(lds_), tiles{p_, reinterpret_cast<int *>(lds_ + NS * kStage), reinterpret_cast<int *>(lds_ + NS * kStage + 64 * 16)} {
+    lane = threadIdx.x & 63;
+    wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    wm = wave / WN;
+    wn = wave % WN;
+    lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)lds;
+    slot = at = 0;
+    left = term = 0;
+  }
+  __device__ __forceinline__ int contraction(const Tile &t) const { return ATR ? t.hi - t.lo : p.K; }
+  // Stages of a term, a whole number of pairs (of zeros where there is nothing to sum).
+  static __device__ __forceinline__ int stages(int klen) { return klen > 0 ? (klen + 2 * kU - 1) / (2 * kU) * 2 : 2; }
+
+  __device__ __forceinline__ void open(const Tile &lt) {
+    const GroupedTerm t = uniform(term) == 0 ? p.t[0] : p.t[1];
+    const int lane = fresh(this->lane);
+#pragma unroll
+    for (int i = 0; i < NA; ++i) {
+      if constexpr (!ATR) {
+        int64_t r = lt.lo + PA::row(wave, lane, i);
+        const bool in = r < lt.hi;
+        if (p.rows) r = p.rows[in ? r : lt.lo];
+        ka[i] = in && r >= 0 && r < p.T ? PA::k_of(lane) : kNone;
+        pa[i] = reinterpret_cast<const char *>(t.A + r * t.lda + PA::k_of(lane));
+      } else {
+        const int k = PA::k_row(wave, lane, i), c = lt.row0 + PA::col(lane, k);
+        ka[i] = c < p.M ? k : kNone;
+        pa[i] = reinterpret_cast<const char *>(t.A + (int64_t)(lt.lo + k) * t.lda + c);
+      }
+    }
+    // (rows and columns that are not the tile's are multiplied as zeros and not stored)
+    const int end = p.N - lt.n0 < 64 * lt.w ? p.N : lt.n0 + 64 * lt.w;
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      const uint16_t *b = t.B + lt.e * t.stride_b;
+      if constexpr (!BTR) {
+        const int n = lt.n0 + PB::row(wave, lane, i);
+        kb[i] = n < end ? PB::k_of(lane) : kNone;
+        pb[i] = reinterpret_cast<const char *>(b + (int64_t)n * t.ldb + PB::k_of(lane));
+      } else {
+        const int k = PB::k_row(wave, lane, i);
+        const int c = lt.n0 + PB::col(lane, k);
+        kb[i] = c < end ? k : kNone;
+        const int64_t row = !ATR ? k : p.rows ? 0 : lt.lo + k;
+        pb[i] = reinterpret_cast<const char *>(b + row * t.ldb + c);
+      }
     }
   }
-  // (offsets that are not ascending can make the sums wrap: no tile then)
-  if (found < 0 || (uint32_t)local >= (uint32_t)(mt * p.tiles_n)) return;
-  found = __builtin_amdgcn_readfirstlane(found);
-  local = __builtin_amdgcn_readfirstlane(local);
-  mt = __builtin_amdgcn_readfirstlane(mt);
-  lo = __builtin_amdgcn_readfirstlane((int)lo);
-  hi = __builtin_amdgcn_readfirstlane((int)hi);
-  // up to 8 row tiles in turn for each column tile
-  const int group = 8 * p.tiles_n, first = local / group * 8, rows = mt - first < 8 ? mt - first : 8;
-  const int in = local % group;
-  const int64_t row0 = lo + (int64_t)BM * (first + in % rows);
-  const int n0 = in / rows * 64 * FN;
-  const int left = (int)((hi - row0 < BM ? hi - row0 : BM) + 63) / 64;
-  if (FM >= 8 && left == 4) tile<T, LAYOUT, FM < 8 ? FM : 8, FN>(p, lds, found, lo, hi, row0, n0);
-  else if (FM >= 6 && left == 3) tile<T, LAYOUT, FM < 6 ? FM : 6, FN>(p, lds, found, lo, hi, row0, n0);
-  else if (FM >= 4 && left == 2) tile<T, LAYOUT, FM < 4 ? FM : 4, FN>(p, lds, found, lo, hi, row0, n0);
-  else tile<T, LAYOUT, 2, FN>(p, lds, found, lo, hi, row0, n0);
-}
+  // TN with a row list: the rows of the next stage (scalar loads: they do not hold up
+  // the vector loads, and each 1 KB load takes few rows).
+  __device__ __forceinline__ void list() {
+    if constexpr (ATR) {
+      if (!p.rows || left <= 0) return;
+      const auto *rows = (const __attribute__((address_space(4))) int *)(uintptr_t)p.rows;
+#pragma unroll
+      for (int i = 0; i < PB::NL; ++i)
+#pragma unroll
+        for (int q = 0; q < kPerRow; ++q) {
+          const int r = end - left + PB::load(wave, i) * kPerRow + q;
+          idx[i * kPerRow + q] = rows[r < end ? r : end - 1];
+        }
+    }
+  }
+  __device__ __forceinline__ void next_tile() {
+    term = 0;
+    left = 0;
+    if (uniform(ahead) == kNoTile) return;
+    Tile t;
+    int n = uniform(next_number);
+    do t = tiles.get(n++);
+    while (t.e != kNoTile && t.w == 0);  // (the last one at most)
+    next_number = n;
+    ahead = t.e == kNoTile ? kNoTile : n - 1;
+    if (t.e == kNoTile) return;
+    end = t.hi;
+    left = contraction(t);
+    open(t);
+  }
+  // The loader's state kept in scalar registers, with the branches made of it.
+  __device__ __forceinline__ void scalar_state() {
+    left = uniform(left);
+    term = uniform(term);
+    ahead = uniform(ahead);
+    next_number = uniform(next_number);
+    end = uniform(end);
+    slot = uniform(slot);
+    at = uniform(at);
+  }
+  // Load n of the next stage (of none: zeros, so that every wave always counts the same).
+  __device__ __forceinline__ void load(int n) {
+    const uint32_t dst = lds0 + slot * kStage;
+    const char *const zeros = reinterpret_cast<const char *>(kZeros);
+#pragma unroll
+    for (int i = 0; i < PA::NL; ++i) {
+      if (i != n) continue;
+      const int j = ATR ? 0 : i;
+      const char *q = ATR ? pa[j] + i * PA::kMore * 2 * p.t[0].lda : pa[j];
+      if (ka[j] + (ATR ? i * PA::kMore : 0) >= left) q = zeros;
+      lds_load(q, dst + PA::load(wave, i) * 1024);
+      if (i + 1 == PA::NL || !ATR) pa[j] += ATR ? p.t[0].lda * (2 * kU) : 2 * kU;
+    }
+#pragma unroll
+    for (int i = 0; i < PB::NL; ++i) {
+      if (i + PA::NL != n) continue;
+      const int j = BTR ? 0 : i;
+      const char *q = pb[j];
+      if (ATR && p.rows) {
+        int r = idx[i * kPerRow];
+#pragma unroll
+        for (int z = 1; z < kPerRow; ++z) r = lane >= z * PB::kRow ? idx[i * kPerRow + z] : r;
+        q = (uint32_t)r < (uint32_t)p.T ? q + (int64_t)r * p.t[0].ldb * 2 : zeros;
+      } else {
+        const int64_t ldb = ATR || uniform(term) == 0 ? p.t[0].ldb : p.t[1].ldb;
+        if (BTR) q += i * PB::kMore * 2 * ldb;
+        if (i + 1 == PB::NL || !BTR) pb[j] += BTR ? ldb * (2 * kU) : 2 * kU;
+      }
+      if (kb[j] + (BTR ? i * PB::kMore : 0) >= left) q = zeros;
+      lds_load(q, dst + BM * kU * 2 + PB::load(wave, i) * 1024);
+    }
+    if (n + 1 < kLoads) return;
+    slot = uniform(slot + 1 == NS ? 0 : slot + 1);
+    left = uniform(left - kU);
+    if (left <= 0 && slot % 2 == 0) {  // a term is a whole number of pairs of stages, and so is NS
+      if (!ATR && uniform(term) + 1 < p.terms && uniform(ahead) != kNoTile) {
+        term = 1;
+        left = p.K;
+        open(tiles.get(ahead));
+      } else {
+        next_tile();
+      }
+      scalar_state();
+    }
+    list();
+  }
 
-template <class T, int FM, int FN>
-__global__ __launch_bounds__(64 * kGroupedWaves) void k_grouped_tn(GroupedParams p) {
+  // The next stage has landed in every wave, and every wave has used what it read of
+  // the stage before the last, whose place takes the loads that follow.  klen: what the
+  // stage holds of its term's contraction (whole, or the odd end).
+  __device__ __forceinline__ uint16_t *enter(int klen) {
+    stage_wait<(NS - 3) * kLoads>();
+    uint16_t *st = reinterpret_cast<uint16_t *>(lds + at * kStage);
+    at = uniform(at + 1 == NS ? 0 : at + 1);
+    if (!(ATR && BTR) && (klen & 7) && klen > 0 && klen < kU) {
+      if (!ATR) zero_tail<64 * WAVES>(st, BM, klen);
+      if (!BTR) zero_tail<64 * WAVES>(st + BM * kU, BN, klen);
+      asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    }
+    return st;
+  }
+
+  // Multiplies out tile number n of the run, of 32 FM rows (or fewer) x 64 FN columns, with
+  // contraction klen, and stores it.
+  template <int FM, int FN>
+  __device__ __forceinline__ void run(int number, int klen) {
+    constexpr int D = FM < 4 ? FM : 4;  // fragments of A held
+    const int lane = fresh(this->lane);
+    f32x4 acc[FM][FN];
+#pragma unroll
+    for (int m = 0; m < FM; ++m)
+#pragma unroll
+      for (int n = 0; n < FN; ++n) acc[m][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+    typename T::frag a[D], b[2][FN];
+    const uint16_t *sa, *sb;
+    auto read_a = [&](int m) { return frag_at<T, ATR, BM>(sa, (wm * FM + m) * 16, lane); };
+    auto read_b = [&](int n) { return frag_at<T, BTR, BN>(sb, (wn * FN + n) * 16, lane); };
+    const int total = stages(klen) * p.terms;
+    {
+      sa = enter(klen);
+      sb = sa + BM * kU;
+#pragma unroll
+      for (int n = 0; n < kLoads; ++n) load(n);
+#pragma unroll
+      for (int n = 0; n < FN; ++n) b[0][n] = read_b(n);
+#pragma unroll
+      for (int m = 0; m < D; ++m) a[m] = read_a(m);
+      int kleft = klen;  // of the stage being multiplied and what follows it in its term
+      for (int j = 0; j < total; j += 2) {
+        const bool more = j + 2 < total;
+#pragma unroll
+        for (int g = 0; g < 2 * FM; ++g) {
+          const int kk = g / FM, m = g % FM;
+          const bool go = kk == 0 || more;  // the tile has a stage after this one
+          if (m == FM - D && go) {
+            kleft -= kU;
+            if (kk == 1 && kleft <= 0) kleft = klen;
+            sa = enter(kleft);
+            sb = sa + BM * kU;
+          }
+          __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+          for (int n = 0; n < FN; ++n) acc[m][n] = T::mfma(b[kk][n], a[g % D], acc[m][n]);
+          __builtin_amdgcn_sched_barrier(0);
+          if (m + D < FM || go) a[g % D] = read_a((m + D) % FM);
+          if (m >= FM - D && go) {
+#pragma unroll
+            for (int n = 0; n < FN; ++n)
+              if (n * D / FN == m - (FM - D)) b[kk ^ 1][n] = read_b(n);
+#pragma unroll
+            for (int n = 0; n < kLoads; ++n)
+              if (n * D / kLoads == m - (FM - D)) load(n);
+          }
+        }
+      }
+    }
+    // lane l holds columns 4 (l / 16) .. + 3 of row l % 16 of each 16 x 16 block
+    const Tile t = tiles.get(number);
+    const int out_lane = fresh(lane), i = out_lane & 15, q4 = out_lane >> 4;
+    const int row0 = ATR ? t.row0 : t.lo, rend = ATR ? p.M : t.hi;
+    uint16_t *C = ATR ? p.C + t.e * p.stride_c : p.C;
+#pragma unroll
+    for (int m = 0; m < FM; ++m) {
+      const int r = row0 + (wm * FM + m) * 16 + i;
+      if (r >= rend) continue;
+#pragma unroll
+      for (int n = 0; n < FN; ++n) {
+        const int c = t.n0 + (wn * FN + n) * 16 + 4 * q4;
+        uint16_t *o = C + (int64_t)r * p.ldc + c;
+        const uint2 v = make_uint2(T::pack(acc[m][n][0], acc[m][n][1]), T::pack(acc[m][n][2], acc[m][n][3]));
+        if (c + 4 <= p.N) {
+          *reinterpret_cast<uint2 *>(o) = v;
+        } else {
+          const uint32_t w[2] = {v.x, v.y};
+          for (int z = 0; c + z < p.N && z < 4; ++z) o[z] = (uint16_t)(w[z >> 1] >> (16 * (z & 1)));
+        }
+      }
+    }
+  }
+
+  // The body for a tile of h x w units of 64.
+  template <int H, int WC>
+  __device__ __forceinline__ bool one_of(int h, int w, int number, int klen) {
+    if constexpr (2 * H <= FMAX && WC <= FNMAX) {
+      if (uniform(h * 8 + w) == H * 8 + WC) {
+        run<2 * H, WC>(number, klen);
+        return true;
+      }
+    }
+    return false;
+  }
+  template <int H>
+  __device__ __forceinline__ void of_height(int h, int w, int number, int klen) {
+    if (!one_of<H, 4>(h, w, number, klen) && !one_of<H, 2>(h, w, number, klen)) one_of<H, 1>(h, w, number, klen);
+  }
+
+  __device__ __forceinline__ void go() {
+    tiles.start(blockIdx.x, gridDim.x, lane);
+    tiles.fill(0, lane);
+    tiles.fill(32, lane);
+    ahead = next_number = end = 0;
+    next_tile();
+    if (ahead == kNoTile) return;  // (the same for every wave: nothing is waited for yet)
+    list();
+#pragma unroll
+    for (int i = 0; i < NS - 2; ++i)
+#pragma unroll
+      for (int n = 0; n < kLoads; ++n) load(n);
+    for (int i = 0;; ++i) {
+      // the loader is less than 32 tiles ahead: the half behind takes the tiles after it
+      if (i > 0 && i % 32 == 0) tiles.fill(i + 32, lane);
+      const Tile t = tiles.get(i);
+      if (t.e == kNoTile) break;
+      scalar_state();
+      const int h = ATR ? FMAX / 2 : uniform((t.hi - t.lo + 63) / 64), w = t.w, klen = contraction(t);
+      if (ATR) of_height<FMAX / 2>(h, w, i, klen);
+      else if (h == 4) of_height<4>(h, w, i, klen);
+      else if (h == 3) of_height<3>(h, w, i, klen);
+      else if (h == 2) of_height<2>(h, w, i, klen);
+      else of_height<1>(h, w, i, klen);
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // none may land in LDS that is another workgroup's by then
+  }
+};
+
+template <class T, int LAYOUT, int WN, int FM, int FN, int NS>
+__global__ __launch_bounds__(128 * WN) void k_grouped(GroupedParams p) {
   extern __shared__ __attribute__((aligned(16))) char lds[];
-  const int t = xcd_tile(blockIdx.x, p.tiles);
-  const int per = p.tiles_m * p.tiles_n, e = t / per, in = t % per;
-  int64_t lo, hi;
-  expert_rows(p, e, lo, hi);
-  const int group = 8 * p.tiles_n, first = in / group * 8, rows = p.tiles_m - first < 8 ? p.tiles_m - first : 8;
-  const int at = in % group;
-  tile<T, DGF_LAYOUT_TN, FM, FN>(p, lds, e, lo, hi, (int64_t)(first + at % rows) * 32 * FM, at / rows * 64 * FN);
+  Stream<T, LAYOUT, WN, FM, FN, NS> s(p, lds);
+  s.go();
 }
 
-template <int FM, int FN>
-constexpr size_t lds_bytes() { return (size_t)2 * (32 * FM + 64 * FN) * kBK * 2; }
-
-template <class T, int FM, int FN>
-hipError_t rows_launch(GroupedParams p, hipStream_t s) {
-  p.tiles_n = (p.N + 64 * FN - 1) / (64 * FN);
-  const int64_t most = p.R / (32 * FM) + (p.R < p.E ? p.R : p.E);  // row tiles, at most
-  p.tiles = (int)(most * p.tiles_n);
-  const dim3 g((uint32_t)p.tiles), b(64 * kGroupedWaves);
-  if (p.layout == DGF_LAYOUT_NT) dgf_launch((k_grouped_rows<T, DGF_LAYOUT_NT, FM, FN>), g, b, lds_bytes<FM, FN>(), s, p);
-  else dgf_launch((k_grouped_rows<T, DGF_LAYOUT_NN, FM, FN>), g, b, lds_bytes<FM, FN>(), s, p);
+template <class T, int LAYOUT, int WN, int FM, int FN, int NS>
+hipError_t grouped_launch(GroupedParams p, int groups, hipStream_t s) {
+  constexpr int BM = 32 * FM, BN = 16 * WN * FN;
+  p.tiles_m = (p.M + BM - 1) / BM;
+  p.tiles_n = (p.N + BN - 1) / BN;
+  dgf_launch((k_grouped<T, LAYOUT, WN, FM, FN, NS>), dim3(groups), dim3(128 * WN), (size_t)NS * (BM + BN) * kU * 2 + Tiles<LAYOUT, BM, BN>::bytes(p.E), s, p);
   return hipGetLastError();
 }
 
-template <class T, int FM, int FN>
-hipError_t tn_launch(GroupedParams p, hipStream_t s) {
-  p.tiles_m = (p.M + 32 * FM - 1) / (32 * FM);
-  p.tiles_n = (p.N + 64 * FN - 1) / (64 * FN);
-  p.tiles = p.tiles_m * p.tiles_n * p.E;
-  dgf_launch((k_grouped_tn<T, FM, FN>), dim3((uint32_t)p.tiles), dim3(64 * kGroupedWaves), lds_bytes<FM, FN>(), s, p);
-  return hipGetLastError();
+template <class T, int LAYOUT>
+hipError_t grouped_l(const GroupedParams &p, hipStream_t s) {
+  const int64_t strips = (p.N + 255) / 256;
+  if (LAYOUT == DGF_LAYOUT_TN) {
+    if ((int64_t)((p.M + 255) / 256) * strips * p.E >= 256) return grouped_launch<T, LAYOUT, 4, 8, 4, 4>(p, 256, s);
+    return grouped_launch<T, LAYOUT, 4, 4, 2, 4>(p, 512, s);
+  }
+  if (p.R / p.E > 64 && p.R / 256 * strips >= 192) return grouped_launch<T, LAYOUT, 4, 8, 4, 4>(p, 256, s);
+  if (p.R / p.E > 64) return grouped_launch<T, LAYOUT, 4, 4, 2, 4>(p, 512, s);
+  return grouped_launch<T, LAYOUT, 4, 2, 2, 6>(p, 512, s);
 }
 
 template <class T>
 hipError_t grouped_t(const GroupedParams &p, hipStream_t s) {
-  if (p.layout == DGF_LAYOUT_TN) {
-    const int64_t big = (int64_t)((p.M + 255) / 256) * ((p.N + 255) / 256) * p.E;
-    return big >= 256 ? tn_launch<T, 8, 4>(p, s) : tn_launch<T, 4, 2>(p, s);
+  switch (p.layout) {
+    case DGF_LAYOUT_NT: return grouped_l<T, DGF_LAYOUT_NT>(p, s);
+    case DGF_LAYOUT_NN: return grouped_l<T, DGF_LAYOUT_NN>(p, s);
+    default: return grouped_l<T, DGF_LAYOUT_TN>(p, s);
   }
-  const int64_t rows = p.R / p.E;
-  if (rows > 64) {
-    const int64_t big = (p.R + 255) / 256 * ((p.N + 255) / 256);
-    return big >= 192 ? rows_launch<T, 8, 4>(p, s) : rows_launch<T, 4, 2>(p, s);
-  }
-  return rows_launch<T, 2, 2>(p, s);
 }
 
 }  // namespace
