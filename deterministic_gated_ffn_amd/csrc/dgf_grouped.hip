@@ -1,6 +1,7 @@
 // Matrix products grouped by expert over ragged rows (gfx950).
 #include "dgf_device.hpp"
 #include "dgf_experts.hpp"
+#include "dgf_rows.hpp"
 
 namespace dgf {
 namespace {
@@ -9,6 +10,7 @@ constexpr int kU = 32;  // contraction elements of a stage
 
 typedef __attribute__((address_space(3))) uint16_t lds_u16;
 typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 __device__ const uint4 kZeros[1] = {};
 
@@ -205,11 +207,12 @@ struct Tiles {
   __device__ __forceinline__ void fill(int i0, int lane) const {
     if (lane >= 32) return;
     const int i = i0 + lane, rounds = count / step, rest = count % step;
-    // parts of a tile of the last round
+    // The last round: its tiles are cut in `split`, if that still leaves one for each.
     const int split = CW >= 4 && rest * 4 <= step ? 4 : CW >= 2 && rest * 2 <= step ? 2 : 1;
-    int at = i * step + place, part = -1;
+    int w = CW, part = 0, at = i * step + place;
     if (i >= rounds) {
       at = rounds * step + place / split;
+      w = CW / split;
       part = place % split;
     }
     int4 v = make_int4(kNoTile, 0, 0, 0);
@@ -229,8 +232,6 @@ struct Tiles {
       if ((uint32_t)c < (uint32_t)tiles_of(hi - lo)) {
         const int group = c / (8 * p.tiles_n) * 8, of = rows - group < 8 ? rows - group : 8, in = c - group * p.tiles_n;
         const int column = in / of, row = group + in % of;
-        const int w = part < 0 ? CW : CW / split;
-        part = part < 0 ? 0 : part;
         if constexpr (!TN) {
           const int even = units / rows, more = units % rows, h = 64 * (even + (row < more));
           lo += 64 * (row * even + (row < more ? row : more));
@@ -278,6 +279,9 @@ struct Stream {
   int ka[NA], kb[NB];  // first k of the piece (kNone: zeros)
   int idx[PB::NL * kPerRow];  // TN with a row list: the next stage's rows
   int at;          // place of the next stage to enter
+  // waits to come that may leave a whole tile's stores (of every wave) under way
+  static constexpr int kStores = FMAX * FNMAX / 2;
+  int stored;
 
   __device__ __forceinline__ Stream(const GroupedParams &p_, char *lds_)
       : p(p_), lds(lds_), tiles{p_, reinterpret_cast<int *>(lds_ + NS * kStage), reinterpret_cast<int *>(lds_ + NS * kStage + 64 * 16)} {
@@ -287,7 +291,7 @@ struct Stream {
     wn = wave % WN;
     lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)lds;
     slot = at = 0;
-    left = term = 0;
+    left = term = stored = 0;
   }
   __device__ __forceinline__ int contraction(const Tile &t) const { return ATR ? t.hi - t.lo : p.K; }
   // Stages of a term, a whole number of pairs (of zeros where there is nothing to sum).
@@ -367,6 +371,7 @@ struct Stream {
     end = uniform(end);
     slot = uniform(slot);
     at = uniform(at);
+    if (ATR) stored = uniform(stored);
   }
   // Load n of the next stage (of none: zeros, so that every wave always counts the same).
   __device__ __forceinline__ void load(int n) {
@@ -419,7 +424,16 @@ struct Stream {
   // the stage before the last, whose place takes the loads that follow.  klen: what the
   // stage holds of its term's contraction (whole, or the odd end).
   __device__ __forceinline__ uint16_t *enter(int klen) {
-    stage_wait<(NS - 3) * kLoads>();
+    // Stores count with the loads, in order: those of the last tile, issued after the
+    // loads of the NS - 2 stages that follow it, need not be done for these to be there.
+    // (TN, whose tiles are short and whose outputs are large: 254 us against 240 at 32768
+    // rows over 128 experts, 768 x 2048.)
+    if (ATR && stored > 0) {
+      stage_wait<(NS - 3) * kLoads + kStores>();
+      stored = uniform(stored - 1);
+    } else {
+      stage_wait<(NS - 3) * kLoads>();
+    }
     uint16_t *st = reinterpret_cast<uint16_t *>(lds + at * kStage);
     at = uniform(at + 1 == NS ? 0 : at + 1);
     if (!(ATR && BTR) && (klen & 7) && klen > 0 && klen < kU) {
@@ -484,28 +498,44 @@ struct Stream {
         }
       }
     }
-    // lane l holds columns 4 (l / 16) .. + 3 of row l % 16 of each 16 x 16 block
+    // Lane l holds columns 4 (l / 16) .. + 3 of row l % 16 of each 16 x 16 block.  Two blocks
+    // side by side trade halves, so that a lane has 8 columns and a store 64 bytes of each
+    // row: half the requests (TN, 32768 rows over 128 experts, 768 x 2048: 209 us against
+    // 240 with 8-byte stores).
     const Tile t = tiles.get(number);
     const int out_lane = fresh(lane), i = out_lane & 15, q4 = out_lane >> 4;
     const int row0 = ATR ? t.row0 : t.lo, rend = ATR ? p.M : t.hi;
-    uint16_t *C = ATR ? p.C + t.e * p.stride_c : p.C;
+    const int r0 = row0 + wm * FM * 16 + i, c0 = t.n0 + wn * FN * 16;
+    uint16_t *o = (ATR ? p.C + t.e * p.stride_c : p.C) + (int64_t)r0 * p.ldc + c0;
+    const bool whole = ATR && FM == FMAX && FN == FNMAX && row0 + 32 * FM <= rend && t.n0 + 64 * FN <= p.N;
 #pragma unroll
     for (int m = 0; m < FM; ++m) {
-      const int r = row0 + (wm * FM + m) * 16 + i;
-      if (r >= rend) continue;
+      if (whole || r0 + 16 * m < rend) {
+        if constexpr (FN % 2 == 0) {
 #pragma unroll
-      for (int n = 0; n < FN; ++n) {
-        const int c = t.n0 + (wn * FN + n) * 16 + 4 * q4;
-        uint16_t *o = C + (int64_t)r * p.ldc + c;
-        const uint2 v = make_uint2(T::pack(acc[m][n][0], acc[m][n][1]), T::pack(acc[m][n][2], acc[m][n][3]));
-        if (c + 4 <= p.N) {
-          *reinterpret_cast<uint2 *>(o) = v;
+          for (int n = 0; n < FN; n += 2) {
+            const uint32_t x[2] = {T::pack(acc[m][n][0], acc[m][n][1]), T::pack(acc[m][n][2], acc[m][n][3])};
+            const uint32_t y[2] = {T::pack(acc[m][n + 1][0], acc[m][n + 1][1]), T::pack(acc[m][n + 1][2], acc[m][n + 1][3])};
+            const u32x2 lo = __builtin_amdgcn_permlane16_swap(x[0], y[0], false, false);
+            const u32x2 hi = __builtin_amdgcn_permlane16_swap(x[1], y[1], false, false);
+            const uint4 v = make_uint4(lo.x, hi.x, lo.y, hi.y);
+            const int c = n * 16 + 16 * (q4 & 1) + 8 * (q4 >> 1);
+            if (whole) *reinterpret_cast<uint4 *>(o + c) = v;
+            else if (c0 + c < p.N) row_st(o, c, p.N - c0, v);
+          }
         } else {
-          const uint32_t w[2] = {v.x, v.y};
-          for (int z = 0; c + z < p.N && z < 4; ++z) o[z] = (uint16_t)(w[z >> 1] >> (16 * (z & 1)));
+          const int c = 4 * q4;
+          const uint32_t w[2] = {T::pack(acc[m][0][0], acc[m][0][1]), T::pack(acc[m][0][2], acc[m][0][3])};
+          if (c0 + c + 4 <= p.N) {
+            *reinterpret_cast<uint2 *>(o + c) = make_uint2(w[0], w[1]);
+          } else {
+            for (int z = 0; c0 + c + z < p.N && z < 4; ++z) o[c + z] = (uint16_t)(w[z >> 1] >> (16 * (z & 1)));
+          }
         }
       }
+      o += 16 * p.ldc;
     }
+    stored = whole ? NS - 2 : 0;
   }
 
   // The body for a tile of h x w units of 64.
