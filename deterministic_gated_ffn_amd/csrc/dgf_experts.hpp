@@ -94,20 +94,20 @@ struct W4Mat {
   const uint16_t *s;
 };
 struct W4Params {
-  const uint16_t *x;    // [M, K] stored type; split: the upper parts in BF16
-  const uint16_t *x2;   // split: the lower parts
+  const uint16_t *x;    // [M, K] stored type; the down product: the activations of launch_w4_gate_up
   int64_t ldx;
   W4Mat w[2];           // one weight, or gate and up
-  uint16_t *y;          // [M, N]; gate/up: the activation's upper parts
-  uint16_t *y2;         // gate/up: its lower parts
+  uint16_t *y;          // [M, N]; gate/up: the activations, w4_act_bytes(M, N)
   int64_t ldy;
   int64_t M;
   int N, K, group, fmt;
 };
+// Bytes of the activations between the FFN's two kernels.
+size_t w4_act_bytes(int64_t M, int I);
 hipError_t launch_pack4(const uint16_t *w, int64_t ldw, uint8_t *q, uint16_t *s, int N, int K, int group, int fmt, hipStream_t st);
 hipError_t launch_unpack4(W4Mat m, uint16_t *w, int64_t ldw, int N, int K, int group, int fmt, hipStream_t st);
 hipError_t launch_w4(const W4Params &p, hipStream_t s);          // y = x w^T
-hipError_t launch_w4_gate_up(const W4Params &p, hipStream_t s);  // a = silu(x w0^T) (x w1^T), as two BF16 parts
-hipError_t launch_w4_down(const W4Params &p, hipStream_t s);     // y = a w^T from the two parts
+hipError_t launch_w4_gate_up(const W4Params &p, hipStream_t s);  // a = silu(x w0^T) (x w1^T)
+hipError_t launch_w4_down(const W4Params &p, hipStream_t s);     // y = a w^T
 
 }  // namespace dgf

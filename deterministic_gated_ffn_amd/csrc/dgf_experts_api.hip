@@ -305,7 +305,7 @@ dgf_status dgf_gemm_w4(const void *x, int64_t ldx, const void *codes, const void
 
 size_t dgf_ffn_fwd_w4_workspace(int64_t M, int64_t H, int64_t I) {
   if (M <= 0 || H <= 0 || I <= 0 || M > kW4MaxM || H >= kMaxLd || I >= kMaxLd) return 0;
-  return 2 * round256((size_t)M * round8(I) * 2);
+  return w4_act_bytes(M, (int)I);
 }
 
 dgf_status dgf_ffn_fwd_w4(const void *x, int64_t ldx, const void *gate_codes, const void *gate_scales,
@@ -324,20 +324,17 @@ dgf_status dgf_ffn_fwd_w4(const void *x, int64_t ldx, const void *gate_codes, co
   const size_t need = dgf_ffn_fwd_w4_workspace(M, H, I);
   if (!ws || ws_bytes < need || !aligned16(ws))
     return fail(DGF_EWORKSPACE, "4-bit forward workspace: need %zu bytes (16-byte aligned), got %zu", need, ws ? ws_bytes : 0);
-  Carve cv{(char *)ws, 0};
-  const int64_t lda = round8(I);
-  uint16_t *hi = cv.take((size_t)M * lda), *lo = cv.take((size_t)M * lda);
   W4Params p{};
   p.x = (const uint16_t *)x; p.ldx = ldx;
   p.w[0] = w4_mat(gate_codes, gate_scales);
   p.w[1] = w4_mat(up_codes, up_scales);
-  p.y = hi; p.y2 = lo; p.ldy = lda;
+  p.y = (uint16_t *)ws;  // the activations
   p.M = M; p.N = (int)I; p.K = (int)H; p.group = (int)group; p.fmt = fmt;
   hipStream_t s = (hipStream_t)stream;
   DGF_TRY(hip_check(timed(s, "4-bit gate/up", [&] { return launch_w4_gate_up(p, s); }), "4-bit gate/up"));
-  p.x = hi; p.x2 = lo; p.ldx = lda;
+  p.x = (const uint16_t *)ws;
   p.w[0] = w4_mat(down_codes, down_scales);
-  p.y = (uint16_t *)y; p.y2 = nullptr; p.ldy = ldy;
+  p.y = (uint16_t *)y; p.ldy = ldy;
   p.N = (int)H; p.K = (int)I;
   DGF_TRY(hip_check(timed(s, "4-bit down", [&] { return launch_w4_down(p, s); }), "4-bit down"));
   return ok();

@@ -1,4 +1,17 @@
 // Products with 4-bit weights and group scales for a few tokens (gfx950).
+//
+//   y[m][n] = sum over groups G of s[n][G] sum over k in G of x[m][k] c[n][k],  |c| <= 7
+//
+// A weight is read once for every 32 tokens, so the codes' bytes are the bound: 4.25 bits a
+// weight with groups of 64.  They are laid out so that a wave reads a tile of 16 rows x 128
+// columns as 1 KB in one piece and has each lane's dwords as it feeds them to the matrix core:
+// two operations turn two codes into two operands 24 + c (the code's bits under the leading
+// one of 16.0), and -24 times the sum of the group's activations, from one more product that
+// all rows share, takes the excess out before the scale.  The group's sum, the scaled sums and
+// those over the waves that share K are FP32.
+// Measured at 4096 x 12288, groups of 64, BF16: gate/up 14.3 us for one token (53 MB, 3.7 TB/s),
+// 23 for 32; down 12.0 and 18.4.  What is left over the copy rate (10 and 5 us) is one start-up
+// of loads and one reduction a workgroup, and past 16 tokens the activations from L2.
 #include "dgf_experts.hpp"
 #include "dgf_rows.hpp"
 
@@ -6,7 +19,7 @@ namespace dgf {
 namespace {
 
 constexpr int kW4Rows = 16, kW4K = 128;  // weights of a tile: 1 KB of codes, 16 bytes a lane
-constexpr int kW4Waves = 8;
+constexpr int kW4Waves = 8;               // that share K
 
 __host__ __device__ inline int w4_tiles_k(int K) { return (K + kW4K - 1) / kW4K; }
 
@@ -113,6 +126,14 @@ __device__ __forceinline__ typename T::frag bias_frag() {  // -24 throughout
   return __builtin_bit_cast(typename T::frag, make_uint4(b, b, b, b));
 }
 
+// Place of the activation (token m, column c, part xp) between the FFN's two kernels: in the
+// order of the down product's fragments, so that each load takes 1 KB in one piece (row by row, rows of 24 KB all start on one L2
+// channel: the down product took 46 us against 18 at 32 tokens).
+__host__ __device__ inline int64_t act_place(int64_t m, int c, int xp, int64_t tiles_m) {
+  const int64_t piece = ((int64_t)(c / kW4K * 2 + xp) * tiles_m + m / 16) * 4 + c % kW4K / 32;
+  return piece * 512 + ((m & 15) + 16 * (c % 32 / 8)) * 8 + c % 8;
+}
+
 // The activation a of a gate/up pair, as two BF16 values whose sum is a to 2^-17.
 __device__ __forceinline__ void split2(float a, uint16_t &hi, uint16_t &lo) {
   hi = f2bf(a);
@@ -120,19 +141,44 @@ __device__ __forceinline__ void split2(float a, uint16_t &hi, uint16_t &lo) {
   lo = h - h == 0.0f ? f2bf(a - h) : 0;
 }
 
-// X: the activations' MFMA type.  S: the scales' (and the output's) type.
-// NT row tiles of the weights a workgroup (PAIR: NT of gate and NT of up), MT
-// tiles of 16 tokens, XP parts the activations come in.
-template <class X, class S, int MT, int NT, int XP, bool PAIR>
+__device__ const uint4 kZeros[1] = {};
+
+// The GS scales of a tile's row, as one load.
+template <class S, int GS>
+struct Scales;
+template <class S>
+struct Scales<S, 1> {
+  uint16_t v;
+  __device__ __forceinline__ float get(int) const { return S::f(v); }
+};
+template <class S>
+struct Scales<S, 2> {
+  uint32_t v;
+  __device__ __forceinline__ float get(int q) const { return q ? S::hi(v) : S::lo(v); }
+};
+template <class S>
+struct Scales<S, 4> {
+  uint2 v;
+  __device__ __forceinline__ float get(int q) const { return q & 1 ? S::hi(q & 2 ? v.y : v.x) : S::lo(q & 2 ? v.y : v.x); }
+};
+
+// X: the activations' MFMA type.  S: the scales' (and the output's) type.  MT tiles of 16
+// tokens, NT row tiles of the weights a workgroup (PAIR: NT of gate and NT of up), XP parts
+// the activations come in (2: as act_place puts them), GS groups a tile, TAIL: K is no
+// multiple of 8, kW4Waves share K: wave z takes the tiles [z n / kW4Waves, (z + 1) n / kW4Waves) of
+// each row, from one that goes by the row tiles: workgroups in step do not all read the same
+// columns of x, which lie on one L2 channel.
+template <class X, class S, int MT, int NT, int XP, bool PAIR, int GS, bool TAIL>
 __global__ __launch_bounds__(64 * kW4Waves) void k_w4(W4Params p) {
   constexpr int W = PAIR ? 2 : 1;
+  constexpr int U = W * NT > 1 ? 2 : 4;  // tiles of codes in flight, and as many multiplied
   extern __shared__ __attribute__((aligned(16))) float red[];  // [waves][W NT MT][4][64]
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int i16 = lane & 15, g = lane >> 4;
   const int tiles_k = w4_tiles_k(p.K), tiles_n = (p.N + kW4Rows - 1) / kW4Rows;
   const int nt0 = blockIdx.x * NT;
   const int64_t m0 = (int64_t)blockIdx.y * 16 * MT;
-  const int gs = kW4K / p.group;  // scales a row and tile
+  const int kt0 = (int)((int64_t)tiles_k * wave / kW4Waves), kt1 = (int)((int64_t)tiles_k * (wave + 1) / kW4Waves);
 
   f32x4 acc[W][NT][MT];
 #pragma unroll
@@ -142,21 +188,31 @@ __global__ __launch_bounds__(64 * kW4Waves) void k_w4(W4Params p) {
 #pragma unroll
       for (int m = 0; m < MT; ++m) acc[w][n][m] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  const typename X::frag bias = bias_frag<X>();
-  for (int kt = wave; kt < tiles_k; kt += kW4Waves) {
-    uint4 code[W][NT];
-    float sc[W][NT][4];
+  struct Codes {
+    uint4 q[W][NT];
+    Scales<S, GS> s[W][NT];
+  };
+  struct Acts {
+    uint4 v[XP][MT][4];
+  };
+  const int share = kt1 - kt0, turn = share > 0 ? nt0 / 6 % share : 0;
+  auto tile = [&](int j) {  // past the wave's last tile: that one again (loaded, not multiplied)
+    j = (j < share ? j : share - 1) + turn;
+    return kt0 + (j < share ? j : j - share);
+  };
+  auto codes = [&](int j, Codes &c) {
+    const int kt = tile(j);
 #pragma unroll
     for (int w = 0; w < W; ++w)
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        const int nt = nt0 + n < tiles_n ? nt0 + n : tiles_n - 1;
-        const int64_t t = (int64_t)nt * tiles_k + kt;
-        code[w][n] = *reinterpret_cast<const uint4 *>(p.w[w].q + (t * 64 + lane) * 16);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) sc[w][n][q] = q < gs ? S::f(p.w[w].s[(t * 16 + i16) * gs + q]) : 0.0f;
+        const int64_t t = (int64_t)(nt0 + n < tiles_n ? nt0 + n : tiles_n - 1) * tiles_k + kt;
+        c.q[w][n] = *reinterpret_cast<const uint4 *>(p.w[w].q + (t * 64 + lane) * 16);
+        c.s[w][n] = *reinterpret_cast<const Scales<S, GS> *>(p.w[w].s + (t * 16 + i16) * GS);
       }
-    uint4 x[XP][MT][4];
+  };
+  auto acts = [&](int j, Acts &x) {
+    const int kt = tile(j);
 #pragma unroll
     for (int xp = 0; xp < XP; ++xp)
 #pragma unroll
@@ -165,22 +221,30 @@ __global__ __launch_bounds__(64 * kW4Waves) void k_w4(W4Params p) {
         for (int i = 0; i < 4; ++i) {
           const int64_t row = m0 + 16 * m + i16;
           const int k = kt * kW4K + 32 * i + 8 * g;
-          x[xp][m][i] = make_uint4(0, 0, 0, 0);
-          if (row < p.M && k < p.K) x[xp][m][i] = row_ld((xp ? p.x2 : p.x) + row * p.ldx, k, p.K);
+          if constexpr (XP == 2) {  // (a token tile past the last: the last again)
+            const int64_t tiles_m = (p.M + 15) / 16, mt = m0 / 16 + m < tiles_m ? m0 / 16 + m : tiles_m - 1;
+            x.v[xp][m][i] = *reinterpret_cast<const uint4 *>(p.x + (((int64_t)(kt * 2 + xp) * tiles_m + mt) * 4 + i) * 512 + lane * 8);
+          } else if constexpr (TAIL) {
+            x.v[xp][m][i] = row < p.M && k < p.K ? row_ld(p.x + row * p.ldx, k, p.K) : make_uint4(0, 0, 0, 0);
+          } else {
+            x.v[xp][m][i] = *(row < p.M && k < p.K ? reinterpret_cast<const uint4 *>(p.x + row * p.ldx + k) : kZeros);
+          }
         }
-    const int per = 4 / gs;  // 32-column parts of a group
+  };
+  const typename X::frag bias = bias_frag<X>();
+  auto multiply = [&](const Codes &c, const Acts &x) {
+    constexpr int kPer = 4 / GS;  // 32-column parts of a group
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      if (q >= gs) break;
+    for (int q = 0; q < GS; ++q) {
+      // -24 times the sum of the group's activations, from which every row's product starts
       f32x4 c0[MT];
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
         c0[m] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (i / per == q)
+        for (int i = q * kPer; i < (q + 1) * kPer; ++i)
 #pragma unroll
-            for (int xp = 0; xp < XP; ++xp) c0[m] = X::mfma(__builtin_bit_cast(typename X::frag, x[xp][m][i]), bias, c0[m]);
+          for (int xp = 0; xp < XP; ++xp) c0[m] = X::mfma(__builtin_bit_cast(typename X::frag, x.v[xp][m][i]), bias, c0[m]);
       }
 #pragma unroll
       for (int w = 0; w < W; ++w)
@@ -190,21 +254,44 @@ __global__ __launch_bounds__(64 * kW4Waves) void k_w4(W4Params p) {
 #pragma unroll
           for (int m = 0; m < MT; ++m) part[m] = c0[m];
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (i / per == q) {
-              const uint32_t word = i == 0 ? code[w][n].x : i == 1 ? code[w][n].y : i == 2 ? code[w][n].z : code[w][n].w;
-              const typename X::frag f = code_frag<X>(word);
+          for (int i = q * kPer; i < (q + 1) * kPer; ++i) {
+            const uint4 &v = c.q[w][n];
+            const typename X::frag f = code_frag<X>(i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w);
 #pragma unroll
-              for (int m = 0; m < MT; ++m)
+            for (int m = 0; m < MT; ++m)
 #pragma unroll
-                for (int xp = 0; xp < XP; ++xp) part[m] = X::mfma(__builtin_bit_cast(typename X::frag, x[xp][m][i]), f, part[m]);
-            }
-          const float s = sc[w][n][q];
+              for (int xp = 0; xp < XP; ++xp) part[m] = X::mfma(__builtin_bit_cast(typename X::frag, x.v[xp][m][i]), f, part[m]);
+          }
+          const float s = c.s[w][n].get(q);
 #pragma unroll
           for (int m = 0; m < MT; ++m)
 #pragma unroll
             for (int e = 0; e < 4; ++e) acc[w][n][m][e] = __builtin_fmaf(s, part[m][e], acc[w][n][m][e]);
         }
+    }
+  };
+
+  if (share > 0) {
+    Codes now[U], next[U];
+    Acts x[2];
+#pragma unroll
+    for (int u = 0; u < U; ++u) codes(u, now[u]);
+    acts(0, x[0]);
+    for (int j = 0; j < share; j += U) {
+      const bool more = j + U < share;
+      if (more) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) codes(j + U + u, next[u]);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (j + u + 1 < share) acts(j + u + 1, x[(u + 1) & 1]);
+        if (j + u < share) multiply(now[u], x[u & 1]);
+      }
+      if (more) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) now[u] = next[u];
+      }
     }
   }
   // the waves' shares of K, added in the waves' order
@@ -218,7 +305,7 @@ __global__ __launch_bounds__(64 * kW4Waves) void k_w4(W4Params p) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) red[((wave * kOut + (w * NT + n) * MT + m) * 4 + e) * 64 + lane] = acc[w][n][m][e];
   __syncthreads();
-  // thread t: value t % 64 of (tile, element) t / 64; its lane's column and row
+  // (tile, element) o of every lane
   for (int o = wave; o < NT * MT * 4; o += kW4Waves) {
     float v[W];
 #pragma unroll
@@ -230,29 +317,69 @@ __global__ __launch_bounds__(64 * kW4Waves) void k_w4(W4Params p) {
     const int e = o & 3, m = (o >> 2) % MT, n = (o >> 2) / MT;
     const int64_t row = m0 + 16 * m + 4 * g + e;
     const int col = (nt0 + n) * kW4Rows + i16;
-    if (row >= p.M || col >= p.N) continue;
+    if (row >= p.M || (!PAIR && col >= p.N)) continue;
     if constexpr (PAIR) {
-      const float sg = 1.0f / (1.0f + expf(-v[0]));
-      split2(v[0] * sg * v[1], p.y[row * p.ldy + col], p.y2[row * p.ldy + col]);
+      const int64_t tiles_m = (p.M + 15) / 16;
+      if (nt0 + n < tiles_n) {
+        const float sg = 1.0f / (1.0f + expf(-v[0]));
+        split2(col < p.N ? v[0] * sg * v[1] : 0.0f, p.y[act_place(row, col, 0, tiles_m)], p.y[act_place(row, col, 1, tiles_m)]);
+      }
+      // the columns that fill up the last tile of the down product are zeros
+      if (nt0 + n == tiles_n - 1)
+        for (int c = col + kW4Rows; c < (tiles_n * kW4Rows + kW4K - 1) / kW4K * kW4K; c += kW4Rows)
+          p.y[act_place(row, c, 0, tiles_m)] = p.y[act_place(row, c, 1, tiles_m)] = 0;
     } else {
       p.y[row * p.ldy + col] = S::r(v[0]);
     }
   }
 }
 
-template <class X, class S, int MT, int NT, int XP, bool PAIR>
+template <class X, class S, int MT, int NT, int XP, bool PAIR, int GS>
 hipError_t w4_launch(const W4Params &p, hipStream_t s) {
   const int tiles_n = (p.N + kW4Rows - 1) / kW4Rows;
   const dim3 g((tiles_n + NT - 1) / NT, (uint32_t)((p.M + 16 * MT - 1) / (16 * MT))), b(64 * kW4Waves);
   const size_t lds = (size_t)kW4Waves * (PAIR ? 2 : 1) * NT * MT * 4 * 64 * 4;
-  dgf_launch((k_w4<X, S, MT, NT, XP, PAIR>), g, b, lds, s, p);
+  if constexpr (XP == 1) {
+    if (p.K % 8) {
+      dgf_launch((k_w4<X, S, MT, NT, XP, PAIR, GS, true>), g, b, lds, s, p);
+      return hipGetLastError();
+    }
+  }
+  dgf_launch((k_w4<X, S, MT, NT, XP, PAIR, GS, false>), g, b, lds, s, p);
   return hipGetLastError();
 }
 
-template <class X, class S, int XP, bool PAIR>
+template <class X, class S, int MT, bool DOWN, bool PAIR, int GS>
+hipError_t w4_n(const W4Params &p, hipStream_t s) {
+  constexpr int XP = DOWN ? 2 : 1;
+  // Up to 16 tokens one row tile a workgroup (gate/up 12288 x 4096, one token: 14.3 us, two
+  // tiles 18.1, three 15.6).  Past that as many as make the least of what its waves read of
+  // the weights and, from L2, of the activations, over the rounds of workgroups (32 tokens:
+  // 31.5 us, 26.7, 23.2).
+  const int tiles = (p.N + kW4Rows - 1) / kW4Rows;
+  int best = 1, cost = 0;
+  for (int n = 1; n <= (MT > 1 ? 3 : 1); ++n) {
+    const int c = (tiles + 256 * n - 1) / (256 * n) * ((PAIR ? 2 : 1) * n + XP * MT);
+    if (n == 1 || c < cost) best = n, cost = c;
+  }
+  if constexpr (MT > 1) {
+    if (best == 3) return w4_launch<X, S, MT, 3, XP, PAIR, GS>(p, s);
+    if (best == 2) return w4_launch<X, S, MT, 2, XP, PAIR, GS>(p, s);
+  }
+  return w4_launch<X, S, MT, 1, XP, PAIR, GS>(p, s);
+}
+// DOWN: the FFN's second product, whose activations are in two parts.
+template <class X, class S, bool DOWN, bool PAIR, int GS>
 hipError_t w4_m(const W4Params &p, hipStream_t s) {
-  if (p.M <= 16) return w4_launch<X, S, 1, 1, XP, PAIR>(p, s);
-  return w4_launch<X, S, 2, PAIR ? 1 : 2, XP, PAIR>(p, s);
+  return p.M <= 16 ? w4_n<X, S, 1, DOWN, PAIR, GS>(p, s) : w4_n<X, S, 2, DOWN, PAIR, GS>(p, s);
+}
+template <class X, class S, bool DOWN, bool PAIR>
+hipError_t w4_g(const W4Params &p, hipStream_t s) {
+  switch (p.group) {
+    case 32: return w4_m<X, S, DOWN, PAIR, 4>(p, s);
+    case 64: return w4_m<X, S, DOWN, PAIR, 2>(p, s);
+    default: return w4_m<X, S, DOWN, PAIR, 1>(p, s);
+  }
 }
 
 }  // namespace
@@ -273,14 +400,16 @@ hipError_t launch_unpack4(W4Mat m, uint16_t *w, int64_t ldw, int N, int K, int g
   return hipGetLastError();
 }
 
+size_t w4_act_bytes(int64_t M, int I) { return (size_t)w4_tiles_k(I) * 2 * ((M + 15) / 16) * 4 * 1024; }
+
 hipError_t launch_w4(const W4Params &p, hipStream_t s) {
-  return p.fmt == FMT_F16 ? w4_m<F16, F16, 1, false>(p, s) : w4_m<Bf16, Bf16, 1, false>(p, s);
+  return p.fmt == FMT_F16 ? w4_g<F16, F16, false, false>(p, s) : w4_g<Bf16, Bf16, false, false>(p, s);
 }
 hipError_t launch_w4_gate_up(const W4Params &p, hipStream_t s) {
-  return p.fmt == FMT_F16 ? w4_m<F16, F16, 1, true>(p, s) : w4_m<Bf16, Bf16, 1, true>(p, s);
+  return p.fmt == FMT_F16 ? w4_g<F16, F16, false, true>(p, s) : w4_g<Bf16, Bf16, false, true>(p, s);
 }
 hipError_t launch_w4_down(const W4Params &p, hipStream_t s) {
-  return p.fmt == FMT_F16 ? w4_m<Bf16, F16, 2, false>(p, s) : w4_m<Bf16, Bf16, 2, false>(p, s);
+  return p.fmt == FMT_F16 ? w4_g<Bf16, F16, true, false>(p, s) : w4_g<Bf16, Bf16, true, false>(p, s);
 }
 
 }  // namespace dgf
