@@ -664,21 +664,21 @@ def _flat_of(t, dtype, shape, device: int, name: str):
     """Pointer of a contiguous tensor of the given type and shape on the device (None: NULL)."""
     if t is None:
         return None
+    if t.dtype is dtype and t.get_device() == device >= 0 and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
     if t.dtype is not dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if device < 0 or t.get_device() != device:
         raise ValueError(f"{name}: expected a GPU tensor of the other operands' device")
-    if t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous tensor of shape {tuple(shape)}, got {tuple(t.shape)}")
-    return t.data_ptr()
+    raise ValueError(f"{name}: expected a contiguous tensor of shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
 def _here(t: torch.Tensor, name: str) -> int:
     """The tensor's device, which has to be the one the call launches on."""
-    if not t.is_cuda:
-        raise ValueError(f"{name}: expected a GPU tensor")
     device = t.get_device()
-    if device != torch.cuda.current_device():
+    if device < 0:
+        raise ValueError(f"{name}: expected a GPU tensor")
+    if device != torch._C._cuda_getDevice():
         raise ValueError(f"{name}: on device {device}, but the call runs on device {torch.cuda.current_device()}")
     return device
 
@@ -740,8 +740,8 @@ def moe_route_bwd(dprobs, logits, ids, probs, renorm: bool = True, stream=None):
         dp = _flat_of(dprobs, torch.float32, (M, k), device, "dprobs")
         ip = _flat_of(ids, torch.int32, (M, k), device, "ids")
         pp = _flat_of(probs, torch.float32, (M, k), device, "probs")
-        d = logits.new_empty((M, E))
-        _check(L.dgf_moe_route_bwd(dp, lp, ld, ip, pp, d.data_ptr(), E, M, E, k, int(renorm), dt, _stream(stream)),
+        d = _empty(M, E, logits)
+        _check(L.dgf_moe_route_bwd(dp, lp, ld, ip, pp, d.data_ptr(), d.stride(0), M, E, k, int(renorm), dt, _stream(stream)),
                "dgf_moe_route_bwd")
     return d
 

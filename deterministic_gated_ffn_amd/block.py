@@ -11,9 +11,17 @@ Training, one layer over tokens [M, H]:
 
 and back through norm_bwd, ffn_bwd_q8 and norm_bwd.  A layer keeps x, h, y, z
 (H wide, 16 bits) and the two checkpoints (I wide, 8.5 bits an element instead
-of 16).  Serving replaces the FFN with moe_fwd.
+of 16).  Serving replaces the FFN with moe_fwd, or with ffn_fwd_w4 (weights in
+4 bits).  A mixture of experts is trained as MoeTrainBlock:
 
-    python -m deterministic_gated_ffn_amd.block       # one training step and one served batch
+    h       = norm(x; w_in)                           norm_fwd
+    l       = h w_router^T                            gemm_tree
+    plan    = k experts a token, rows by expert       moe_route
+    g, u    = h W_gate,e^T, h W_up,e^T                gemm_grouped (rows of h by the plan's list)
+    o       = silu(g) u W_down,e^T                    act_fwd, gemm_grouped
+    z       = x + dropout(sum of p_j o_j)             moe_combine, dropout
+
+    python -m deterministic_gated_ffn_amd.block       # training steps and served batches
 """
 from __future__ import annotations
 
@@ -69,6 +77,65 @@ class MoeBlock:
         return (r["z"], r["h"]) if w_next is not None else r["z"]
 
 
+class FfnBlock4:
+    """z = alpha x + gate norm(FFN(norm(x))) for a few tokens, the FFN's weights in 4 bits (pack4)."""
+
+    def __init__(self, w_in, w_gate, w_up, w_down, w_out, group: int = 64, gate=None, alpha: float = 1.0,
+                 eps: float = 1e-6):
+        self.w_in, self.w_out, self.gate, self.alpha, self.eps = w_in, w_out, gate, alpha, eps
+        self.w = tuple(dgf.pack4(w, group=group) for w in (w_gate, w_up, w_down))
+
+    def __call__(self, x, stream=None):
+        h = dgf.norm_fwd(x, w_next=self.w_in, eps=self.eps, stream=stream)["h"]
+        y = dgf.ffn_fwd_w4(h, *self.w, stream=stream)
+        return dgf.norm_fwd(x, y, w_post=self.w_out, gate=self.gate, alpha=self.alpha, eps=self.eps, stream=stream)["z"]
+
+
+class MoeTrainBlock:
+    """z = x + dropout(MoE(norm(x))) over any number of tokens, forward and backward.
+    I and H are multiples of 8; a token whose logits are all -inf goes nowhere."""
+
+    def __init__(self, w_in, w_router, w_gate, w_up, w_down, top_k: int, p_drop: float = 0.0, renorm: bool = True,
+                 eps: float = 1e-6):
+        self.w_in, self.w_router, self.w_gate, self.w_up, self.w_down = w_in, w_router, w_gate, w_up, w_down
+        self.top_k, self.p_drop, self.renorm, self.eps = top_k, p_drop, renorm, eps
+
+    def forward(self, x, rng, stream=None):
+        """Returns z and what the backward needs; rng (seed, step) as dropout takes it,
+        to be as it is now when the backward runs."""
+        pre = dgf.norm_fwd(x, w_next=self.w_in, eps=self.eps, training=True, stream=stream)
+        h = pre["h"]
+        logits = dgf.gemm_tree("NT", h, self.w_router, stream=stream)
+        plan = dgf.moe_route(logits, self.top_k, renorm=self.renorm, stream=stream)
+        g = dgf.gemm_grouped("NT", h, self.w_gate, plan.offsets, rows=plan.rows, stream=stream)
+        u = dgf.gemm_grouped("NT", h, self.w_up, plan.offsets, rows=plan.rows, stream=stream)
+        a = dgf.act_fwd(g, u, stream=stream)
+        o = dgf.gemm_grouped("NT", a, self.w_down, plan.offsets, stream=stream)
+        y = dgf.moe_combine(o, plan.pos, plan.probs, stream=stream)
+        z = dgf.dropout(y, self.p_drop, rng, res=x, stream=stream)
+        return z, (x, h, pre["rstd"], logits, plan, g, u, a, o, rng)
+
+    def backward(self, dz, saved, stream=None):
+        """Gradients of the block's parameters, and dx."""
+        x, h, rstd, logits, plan, g, u, a, o, rng = saved
+        off, rows = plan.offsets, plan.rows
+        dy = dgf.dropout(dz, self.p_drop, rng, stream=stream)
+        do, dprobs = dgf.moe_combine_bwd(dy, o, plan.pos, plan.probs, stream=stream)
+        da = dgf.gemm_grouped("NN", do, self.w_down, off, stream=stream)
+        dg, du, _ = dgf.act_bwd(da, g, u, stream=stream)
+        # the gate and up lanes of a row in one sum, then the rows of a token
+        dh = dgf.moe_combine(dgf.gemm_grouped("NN", dg, self.w_gate, off, add=(du, self.w_up), stream=stream), plan.pos,
+                             stream=stream)
+        dlogits = dgf.moe_route_bwd(dprobs, logits, plan.ids, plan.probs, renorm=self.renorm, stream=stream)
+        # (p = 0 keeps everything: the router's share of dh added to the experts')
+        dh = dgf.dropout(dgf.gemm_tree("NN", dlogits, self.w_router, stream=stream), 0.0, rng, res=dh, stream=stream)
+        pre = dgf.norm_bwd(dz, dh, x, w_next=self.w_in, rstd=rstd, stream=stream)
+        return {"dx": pre["dres"], "dw_in": pre["dw_next"], "dw_router": dgf.gemm_tree("TN", dlogits, h, stream=stream),
+                "dW_gate": dgf.gemm_grouped("TN", dg, h, off, rows=rows, stream=stream),
+                "dW_up": dgf.gemm_grouped("TN", du, h, off, rows=rows, stream=stream),
+                "dW_down": dgf.gemm_grouped("TN", do, a, off, stream=stream)}
+
+
 def _demo(M: int = 512, H: int = 1024, I: int = 4096, E: int = 16, k: int = 2) -> None:
     gen = torch.Generator(device="cuda").manual_seed(0)
 
@@ -85,11 +152,18 @@ def _demo(M: int = 512, H: int = 1024, I: int = 4096, E: int = 16, k: int = 2) -
     kept = sum(t.codes.nbytes + t.scales.nbytes for t in (saved[4], saved[5]))
     print(f"training step, {M} tokens: |z| = {z.float().norm().item():.1f}, |dx| = {grads['dx'].float().norm().item():.2f}, "
           f"g and u kept in {kept / 1e6:.2f} MB instead of {4 * M * I / 1e6:.2f}")
-    moe = MoeBlock(ones(), rand(E, H, scale=0.05), rand(E, I, H, scale=0.02), rand(E, I, H, scale=0.02),
-                   rand(E, H, I, scale=0.02), ones(), k)
+    experts = (rand(E, H, scale=0.05), rand(E, I, H, scale=0.02), rand(E, I, H, scale=0.02), rand(E, H, I, scale=0.02))
+    train = MoeTrainBlock(ones(), *experts, k, p_drop=0.1)
+    z, saved = train.forward(x, torch.tensor([1, 0], device="cuda"))
+    grads = train.backward(rand(M, H, scale=0.1), saved)
+    print(f"training step of a mixture, {M} tokens over {k} of {E} experts: |z| = {z.float().norm().item():.1f}, "
+          f"|dx| = {grads['dx'].float().norm().item():.2f}, |dW_gate| = {grads['dW_gate'].float().norm().item():.2f}")
+    moe = MoeBlock(ones(), *experts, ones(), k)
     z, h = moe(x[:8], w_next=ones())
     print(f"served batch, 8 tokens over {k} of {E} experts: |z| = {z.float().norm().item():.1f}, "
           f"|h| = {h.float().norm().item():.1f}")
+    z = FfnBlock4(ones(), *block.w, ones())(x[:8])
+    print(f"served batch, 8 tokens, weights in 4 bits: |z| = {z.float().norm().item():.1f}")
 
 
 if __name__ == "__main__":
