@@ -27,7 +27,7 @@ struct GroupedParams {
   int64_t R;
   int M, N, K, E;       // TN: M x N outputs an expert; NT, NN: N columns, K the contraction
   int layout, fmt;
-  int tiles_m, tiles_n, tiles;  // set by the launch
+  int tiles_m, tiles_n;  // of one expert's matrix (NT, NN: columns only), set by the launch
 };
 hipError_t launch_grouped(const GroupedParams &p, hipStream_t s);
 

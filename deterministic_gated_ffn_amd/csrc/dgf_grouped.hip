@@ -183,7 +183,8 @@ struct Tiles {
     }
     return v;
   }
-  // The first tile that begins at cost `from` or later, e's costs starting at `before`.
+  // Sums up the tiles and finds the XCD's run: from the first tile that begins at its share of
+  // the cost or later (within an expert, all cost the same).
   __device__ __forceinline__ void start(int b, int n, int lane) {
     int64_t all = 0;
     int tiles = 0;
@@ -451,8 +452,8 @@ struct Stream {
   __device__ __forceinline__ uint16_t *enter(int klen) {
     // Stores count with the loads, in order: those of the last tile, issued after the
     // loads of the NS - 2 stages that follow it, need not be done for these to be there.
-    // (TN, whose tiles are short and whose outputs are large: 254 us against 240 at 32768
-    // rows over 128 experts, 768 x 2048.)
+    // (TN only, whose tiles are short and whose outputs are large: 32768 rows over 128 experts,
+    // 768 x 2048, then with 8-byte stores: 240 us, 254 when every store was waited for.)
     if (ATR && stored > 0) {
       stage_wait<(NS - 3) * kLoads + kStores>();
       stored = uniform(stored - 1);
@@ -592,8 +593,10 @@ struct Stream {
 #pragma unroll
       for (int n = 0; n < kLoads; ++n) load(n);
     for (int i = 0;; ++i) {
-      // the loader is less than 32 tiles ahead: the half behind takes the tiles after it
-      if (i > 0 && i % 32 == 0) tiles.fill(i + 32, lane);
+      // The half behind takes the tiles after it.  Waves are at most one tile apart (a barrier
+      // a stage) and the loader a few ahead: after 8 tiles none looks at that half any more,
+      // and none yet at the next.
+      if (i >= 40 && i % 32 == 8) tiles.fill(i + 24, lane);
       const Tile t = tiles.get(i);
       if (t.e == kNoTile) break;
       scalar_state();

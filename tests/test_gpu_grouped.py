@@ -99,6 +99,23 @@ def test_large_tiles(dtype, layout):
     check(got, ref, mags, max(counts) if layout == "TN" else 456)
 
 
+@pytest.mark.parametrize("layout,M,N,K,rows", [("NT", 0, 4000, 8, 1), ("NN", 0, 4000, 40, 1), ("TN", 520, 530, 0, 3),
+                                               ("NT", 0, 9300, 8, 70)])
+def test_many_tiles_each(layout, M, N, K, rows):
+    """1024 experts of a few rows and many columns: 40 and more tiles for a workgroup."""
+    gen = torch.Generator(device="cuda").manual_seed(8)
+    E = 1024 if rows < 70 else 256
+    off = list(range(0, E * rows + 1, rows))
+    A, B = make(layout, off, E * rows, M, N, K, torch.bfloat16, gen)
+    got = dgf.gemm_grouped(layout, A, B, ints(*off))
+    assert torch.equal(got, dgf.gemm_grouped(layout, A, B, ints(*off)))
+    for e in range(0, E, 8):  # (in parts: FP64 takes four times the memory)
+        o = [x - off[e] for x in off[e:e + 9]]
+        a, b = A[off[e]:off[e + 8]], (B[off[e]:off[e + 8]] if layout == "TN" else B[e:e + 8])
+        ref, mags = reference(layout, a, b, o, None)
+        check(got[e:e + 8] if layout == "TN" else got[off[e]:off[e + 8]], ref, mags, rows if layout == "TN" else K)
+
+
 @pytest.mark.parametrize("layout", ["NT", "NN"])
 @pytest.mark.parametrize("K", [0, 5, 64, 100, 513])
 @pytest.mark.parametrize("listed", [False, True])
