@@ -1,4 +1,14 @@
 // Dropout from a counter-based generator, with the residual (gfx950).
+//
+//   z = alpha res + (draw >= cut ? x / (1 - cut / 65536) : 0)
+//
+// The mask is a function of the seed, the step and the value's place, so that it is neither
+// written nor read: a call moves x, res and z only, which bounds it.  A thread takes 8 columns
+// of a row and draws 16 bits for each of them, all from one block of the generator: a
+// probability is a multiple of 2^-16 (0.1 is off by 6e-6), and half the 32-bit products
+// that a draw of 32 bits would take.  x / (1 - p) and the sum are FP32, rounded once.
+// Measured, BF16: 4096 x 4096 with the residual 16.1 us (100 MB, 6.2 TB/s: part of it comes
+// from cache, at the rate of a copy 19.5); 1003 x 5125 without 6.5 us.
 #include "dgf_experts.hpp"
 #include "dgf_rows.hpp"
 
@@ -22,7 +32,7 @@ __device__ __forceinline__ void philox(uint32_t (&c)[4], uint32_t k0, uint32_t k
 
 template <class T, bool RES>
 __global__ __launch_bounds__(256) void k_dropout(DropoutParams p) {
-  const int64_t per = (p.H + 7) / 8, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t per = (p.H + 7) / 8, i = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 256 + threadIdx.x;
   if (i >= p.M * per) return;
   const int64_t m = i / per, col = 8 * (i - m * per);
   const uint64_t seed = (uint64_t)p.rng[0], step = (uint64_t)p.rng[1];
@@ -49,7 +59,10 @@ __global__ __launch_bounds__(256) void k_dropout(DropoutParams p) {
 
 template <class T>
 hipError_t dropout_t(const DropoutParams &p, hipStream_t s) {
-  const dim3 g((uint32_t)((p.M * ((p.H + 7) / 8) + 255) / 256)), b(256);
+  // (2^32 threads are more than one dimension of a grid takes)
+  constexpr int64_t kX = (int64_t)1 << 23;
+  const int64_t blocks = (p.M * ((p.H + 7) / 8) + 255) / 256;
+  const dim3 g((uint32_t)(blocks < kX ? blocks : kX), (uint32_t)((blocks + kX - 1) / kX)), b(256);
   if (p.res) dgf_launch((k_dropout<T, true>), g, b, 0, s, p);
   else dgf_launch((k_dropout<T, false>), g, b, 0, s, p);
   return hipGetLastError();

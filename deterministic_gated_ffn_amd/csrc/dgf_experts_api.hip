@@ -61,6 +61,13 @@ dgf_status check_w4_dims(int64_t M, int64_t N, int64_t K, int64_t group) {
   return DGF_OK;
 }
 
+// Packing has a wave for each tile of 16 x 128, one grid for all of them.
+dgf_status check_tiles4(int64_t N, int64_t K) {
+  if ((N + 15) / 16 * ((K + 127) / 128) > ((int64_t)1 << 26) - 4)
+    return fail(DGF_EUNSUPPORTED, "4-bit weights: more than 2^26 tiles of 16 x 128 (N=%lld K=%lld)", (long long)N, (long long)K);
+  return DGF_OK;
+}
+
 dgf_status check_w4(const char *name, const void *codes, const void *scales) {
   if (!codes || !scales) return fail(DGF_EINVAL, "%s: the %s are NULL", name, codes ? "scales" : "codes");
   if (!aligned16(codes)) return fail(DGF_EINVAL, "%s: the codes are not 16-byte aligned", name);
@@ -261,6 +268,7 @@ dgf_status dgf_pack4(const void *w, int64_t ldw, void *codes, void *scales, int6
   int fmt = 0;
   DGF_TRY(stored_type(dtype, &fmt));
   DGF_TRY(check_w4_dims(0, N, K, group));
+  DGF_TRY(check_tiles4(N, K));
   DGF_TRY(check_mat("w", w, ldw, N, K));
   DGF_TRY(check_w4("w4", codes, scales));
   hipStream_t s = (hipStream_t)stream;
@@ -275,6 +283,7 @@ dgf_status dgf_unpack4(const void *codes, const void *scales, void *w, int64_t l
   int fmt = 0;
   DGF_TRY(stored_type(dtype, &fmt));
   DGF_TRY(check_w4_dims(0, N, K, group));
+  DGF_TRY(check_tiles4(N, K));
   DGF_TRY(check_w4("w4", codes, scales));
   DGF_TRY(check_mat("w", w, ldw, N, K));
   hipStream_t s = (hipStream_t)stream;

@@ -438,7 +438,7 @@ dgf_status dgf_dropout(const void *x, int64_t ldx, const void *res, int64_t ld_r
  * tile, 16-byte aligned: dword 4 l + i of tile lane l holds row l % 16, columns
  * 32 i + 8 (l / 16) + 0..7, column 2 d in bits 4 d.. and 2 d + 1 in bits 16 + 4 d..,
  * as c + 8; scales, 16 x 128/group a tile, row-major, stored type, 8-byte aligned.
- * Rows and columns past N and K are codes of 0.
+ * Rows and columns past N and K are codes of 0.  At most 2^26 - 4 tiles.
  */
 dgf_status dgf_pack4(const void *w, int64_t ldw, void *codes, void *scales, int64_t N, int64_t K, int64_t group, int dtype,
                      void *stream);
@@ -450,7 +450,8 @@ dgf_status dgf_unpack4(const void *codes, const void *scales, void *w, int64_t l
  * (W_up x)) with all three.  Made for a few tokens: the weights are read once for
  * every 32.  Sums are FP32 in an order that does not depend on M; y is rounded
  * once; the activation passes between the FFN's two kernels to 2^-16 of its value.
- * Inputs are finite.  M <= 65536.  Workspace: dgf_ffn_fwd_w4_workspace bytes.
+ * Inputs, and the FFN's activations, are finite and below 2^110 (a group's sum
+ * passes through 24 times the sum of its inputs).  M <= 65536.  Workspace: dgf_ffn_fwd_w4_workspace bytes.
  */
 dgf_status dgf_gemm_w4(const void *x, int64_t ldx, const void *codes, const void *scales, void *y, int64_t ldy, int64_t M,
                        int64_t N, int64_t K, int64_t group, int dtype, void *stream);

@@ -125,7 +125,8 @@ def test_4_bit_refusals(lib):
     bad = ((dict(group=48), EINVAL, b"group=48"), (dict(group=0), EINVAL, b"group=0"), (dict(N=0), EINVAL, b"rows and columns"),
            (dict(K=0), EINVAL, b"rows and columns"), (dict(w=None), EINVAL, b"w is NULL"), (dict(codes=None), EINVAL, b"codes"),
            (dict(scales=None), EINVAL, b"scales"), (dict(codes=FAKE + 8), EINVAL, b"codes"), (dict(scales=FAKE + 4), EINVAL, b"scales"),
-           (dict(ldw=120), EINVAL, b"w: leading"), (dict(dtype=2), EUNSUPPORTED, b"FP32"), (dict(K=1 << 23), EUNSUPPORTED, b"2^23"))
+           (dict(ldw=120), EINVAL, b"w: leading"), (dict(dtype=2), EUNSUPPORTED, b"FP32"), (dict(K=1 << 23), EUNSUPPORTED, b"2^23"),
+           (dict(N=1 << 19, K=1 << 18, ldw=1 << 18), EUNSUPPORTED, b"2^26 tiles"))
     check(lib, lib.dgf_pack4, names, d, bad)
     check(lib, lib.dgf_unpack4, "codes scales w ldw N K group dtype stream", d, bad)
     d = dict(x=FAKE, ldx=128, codes=FAKE, scales=FAKE, y=FAKE, ldy=32, M=3, N=32, K=128, group=64, dtype=BF, stream=None)

@@ -10,10 +10,11 @@ pytestmark = pytest.mark.gpu
 BF, FH = torch.bfloat16, torch.float16
 
 
-def philox(seed, step, n):
-    """Philox-4x32-10 (Salmon et al. 2011) at counters {0..n-1, step}, [n, 4] words."""
+def philox(seed, step, n, first=0):
+    """Philox-4x32-10 (Salmon et al. 2011) at counters {first..first+n-1, step}, [n, 4] words."""
     c = np.zeros((4, n), dtype=np.uint64)
-    c[0], c[1] = np.arange(n) & 0xFFFFFFFF, np.arange(n) >> 32
+    at = np.arange(first, first + n)
+    c[0], c[1] = at & 0xFFFFFFFF, at >> 32
     c[2], c[3] = step & 0xFFFFFFFF, step >> 32 & 0xFFFFFFFF
     k0, k1 = seed & 0xFFFFFFFF, seed >> 32 & 0xFFFFFFFF
     for _ in range(10):
@@ -126,3 +127,15 @@ def test_replays_draw_new_masks():
         assert torch.equal(z, want)
         seen.append(z.clone())
     assert not torch.equal(seen[0], seen[1])
+
+
+def test_more_than_2_to_the_32_pieces():
+    """Rows on both sides of the 2^32nd piece of 8 values, in place: the mask goes on with the counter's second word."""
+    M, H = 1 << 21, 16392
+    x = torch.ones(M, H, dtype=BF, device="cuda")
+    dgf.dropout(x, 0.5, rng_of(5, 6), out=x)
+    per = H // 8
+    for m in (0, (1 << 32) // per - 1, (1 << 32) // per, (1 << 32) // per + 1, M - 1):
+        words = philox(5, 6, per, m * per)
+        keep = torch.from_numpy((np.stack([words & 0xFFFF, words >> 16], 2).reshape(-1) >= 32768)).cuda()
+        assert torch.equal(x[m], torch.where(keep, 2.0, 0.0).to(BF)), m
