@@ -9,9 +9,11 @@
 // one of 16.0), and -24 times the sum of the group's activations, from one more product that
 // all rows share, takes the excess out before the scale.  The group's sum, the scaled sums and
 // those over the waves that share K are FP32.
-// Measured at 4096 x 12288, groups of 64, BF16: gate/up 14.3 us for one token (53 MB, 3.7 TB/s),
-// 23 for 32; down 12.0 and 18.4.  What is left over the copy rate (10 and 5 us) is one start-up
-// of loads and one reduction a workgroup, and past 16 tokens the activations from L2.
+// Measured at 4096 x 12288, groups of 64, BF16: gate/up 12.4 us for one token (53 MB, 4.3 TB/s),
+// 16.4 for 32; down 11.5 and 17.6.  What is left over the copy rate (10 and 5 us) is one start-up
+// of loads and one reduction a workgroup, and past 16 tokens the activations: each of the down
+// product's 256 workgroups reads all 1.5 MB of them from L2, 400 MB.  (Four workgroups that share
+// K and four times the rows, with a launch that adds them: 22 us.)
 #include "dgf_experts.hpp"
 #include "dgf_rows.hpp"
 
@@ -171,7 +173,12 @@ struct Scales<S, 4> {
 template <class X, class S, int MT, int NT, int XP, bool PAIR, int GS, bool TAIL>
 __global__ __launch_bounds__(64 * kW4Waves) void k_w4(W4Params p) {
   constexpr int W = PAIR ? 2 : 1;
-  constexpr int U = W * NT > 1 ? 2 : 4;  // tiles of codes in flight, and as many multiplied
+  // Tiles in a ring of registers: each is loaded anew as soon as it has been used, so that all
+  // but one are on their way.  At 4096 x 12288 against activations one tile ahead and codes two
+  // or four: gate/up 12.4 us against 14.4 for one token and 16.4 against 23.1 for 32, down 11.5
+  // against 12.1 and 17.6 against 19.7.  (Gate/up, one token, 4: 15.5 us, fewer waves fit.
+  // TAIL's loads take more registers.)
+  constexpr int R = MT > 1 ? (TAIL ? 1 : 2) : PAIR || TAIL ? 2 : 4;
   extern __shared__ __attribute__((aligned(16))) float red[];  // [waves][W NT MT][4][64]
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int i16 = lane & 15, g = lane >> 4;
@@ -192,8 +199,8 @@ __global__ __launch_bounds__(64 * kW4Waves) void k_w4(W4Params p) {
     uint4 q[W][NT];
     Scales<S, GS> s[W][NT];
   };
-  struct Acts {
-    uint4 v[XP][MT][4];
+  struct Acts {  // of half a tile
+    uint4 v[XP][MT][2];
   };
   const int share = kt1 - kt0, turn = share > 0 ? nt0 / 6 % share : 0;
   auto tile = [&](int j) {  // past the wave's last tile: that one again (loaded, not multiplied)
@@ -211,19 +218,19 @@ __global__ __launch_bounds__(64 * kW4Waves) void k_w4(W4Params p) {
         c.s[w][n] = *reinterpret_cast<const Scales<S, GS> *>(p.w[w].s + (t * 16 + i16) * GS);
       }
   };
-  auto acts = [&](int j, Acts &x) {
+  auto acts = [&](int j, int h, Acts &x) {
     const int kt = tile(j);
 #pragma unroll
     for (int xp = 0; xp < XP; ++xp)
 #pragma unroll
       for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 2; ++i) {
           const int64_t row = m0 + 16 * m + i16;
-          const int k = kt * kW4K + 32 * i + 8 * g;
+          const int k = kt * kW4K + 64 * h + 32 * i + 8 * g;
           if constexpr (XP == 2) {  // (a token tile past the last: the last again)
             const int64_t tiles_m = (p.M + 15) / 16, mt = m0 / 16 + m < tiles_m ? m0 / 16 + m : tiles_m - 1;
-            x.v[xp][m][i] = *reinterpret_cast<const uint4 *>(p.x + (((int64_t)(kt * 2 + xp) * tiles_m + mt) * 4 + i) * 512 + lane * 8);
+            x.v[xp][m][i] = *reinterpret_cast<const uint4 *>(p.x + (((int64_t)(kt * 2 + xp) * tiles_m + mt) * 4 + 2 * h + i) * 512 + lane * 8);
           } else if constexpr (TAIL) {
             x.v[xp][m][i] = row < p.M && k < p.K ? row_ld(p.x + row * p.ldx, k, p.K) : make_uint4(0, 0, 0, 0);
           } else {
@@ -232,17 +239,18 @@ __global__ __launch_bounds__(64 * kW4Waves) void k_w4(W4Params p) {
         }
   };
   const typename X::frag bias = bias_frag<X>();
-  auto multiply = [&](const Codes &c, const Acts &x) {
-    constexpr int kPer = 4 / GS;  // 32-column parts of a group
+  // Half h of a tile.  (A group of 128 columns is scaled in two halves.)
+  auto multiply = [&](const Codes &c, const Acts &x, int h) {
+    constexpr int kPer = GS == 4 ? 1 : 2;  // 32-column parts with one scale
 #pragma unroll
-    for (int q = 0; q < GS; ++q) {
-      // -24 times the sum of the group's activations, from which every row's product starts
+    for (int q = 0; q < 2; q += kPer) {
+      // -24 times the sum of their activations, from which every row's product starts
       f32x4 c0[MT];
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
         c0[m] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int i = q * kPer; i < (q + 1) * kPer; ++i)
+        for (int i = q; i < q + kPer; ++i)
 #pragma unroll
           for (int xp = 0; xp < XP; ++xp) c0[m] = X::mfma(__builtin_bit_cast(typename X::frag, x.v[xp][m][i]), bias, c0[m]);
       }
@@ -254,15 +262,15 @@ __global__ __launch_bounds__(64 * kW4Waves) void k_w4(W4Params p) {
 #pragma unroll
           for (int m = 0; m < MT; ++m) part[m] = c0[m];
 #pragma unroll
-          for (int i = q * kPer; i < (q + 1) * kPer; ++i) {
+          for (int i = q; i < q + kPer; ++i) {
             const uint4 &v = c.q[w][n];
-            const typename X::frag f = code_frag<X>(i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w);
+            const typename X::frag f = code_frag<X>(h ? (i ? v.w : v.z) : i ? v.y : v.x);
 #pragma unroll
             for (int m = 0; m < MT; ++m)
 #pragma unroll
               for (int xp = 0; xp < XP; ++xp) part[m] = X::mfma(__builtin_bit_cast(typename X::frag, x.v[xp][m][i]), f, part[m]);
           }
-          const float s = c.s[w][n].get(q);
+          const float s = c.s[w][n].get((2 * h + q) * GS / 4);
 #pragma unroll
           for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -272,27 +280,37 @@ __global__ __launch_bounds__(64 * kW4Waves) void k_w4(W4Params p) {
   };
 
   if (share > 0) {
-    Codes now[U], next[U];
-    Acts x[2];
+    Codes c[R];
+    Acts x[R][2];
 #pragma unroll
-    for (int u = 0; u < U; ++u) codes(u, now[u]);
-    acts(0, x[0]);
-    for (int j = 0; j < share; j += U) {
-      const bool more = j + U < share;
-      if (more) {
+    for (int u = 0; u < R; ++u) {
+      codes(u, c[u]);
+      acts(u, 0, x[u][0]);
+      acts(u, 1, x[u][1]);
+    }
+    int j = 0;
+    for (; j + R < share; j += R) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) codes(j + U + u, next[u]);
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (j + u + 1 < share) acts(j + u + 1, x[(u + 1) & 1]);
-        if (j + u < share) multiply(now[u], x[u & 1]);
-      }
-      if (more) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) now[u] = next[u];
+      for (int u = 0; u < R; ++u) {
+        // (the barriers keep every load where it is: moved up, they cost spilled registers)
+        multiply(c[u], x[u][0], 0);
+        __builtin_amdgcn_sched_barrier(0);
+        acts(j + R + u, 0, x[u][0]);
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(c[u], x[u][1], 1);
+        __builtin_amdgcn_sched_barrier(0);
+        acts(j + R + u, 1, x[u][1]);
+        __builtin_amdgcn_sched_barrier(0);
+        codes(j + R + u, c[u]);
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
+#pragma unroll
+    for (int u = 0; u < R; ++u)
+      if (j + u < share) {
+        multiply(c[u], x[u][0], 0);
+        multiply(c[u], x[u][1], 1);
+      }
   }
   // the waves' shares of K, added in the waves' order
   constexpr int kOut = W * NT * MT;
@@ -352,10 +370,10 @@ hipError_t w4_launch(const W4Params &p, hipStream_t s) {
 template <class X, class S, int MT, bool DOWN, bool PAIR, int GS>
 hipError_t w4_n(const W4Params &p, hipStream_t s) {
   constexpr int XP = DOWN ? 2 : 1;
-  // Up to 16 tokens one row tile a workgroup (gate/up 12288 x 4096, one token: 14.3 us, two
-  // tiles 18.1, three 15.6).  Past that as many as make the least of what its waves read of
-  // the weights and, from L2, of the activations, over the rounds of workgroups (32 tokens:
-  // 31.5 us, 26.7, 23.2).
+  // Up to 16 tokens one row tile a workgroup (gate/up 12288 x 4096, one token, with less in
+  // flight than now: 14.3 us, two tiles 18.1, three 15.6).  Past that as many as make the least
+  // of what its waves read of the weights and, from L2, of the activations, over the rounds of
+  // workgroups (32 tokens, likewise: 31.5 us, 26.7, 23.2).
   const int tiles = (p.N + kW4Rows - 1) / kW4Rows;
   int best = 1, cost = 0;
   for (int n = 1; n <= (MT > 1 ? 3 : 1); ++n) {
