@@ -36,6 +36,45 @@ def make(M, H, I, E, seed=0):
     return w, rand(gen, M, H), rand(gen, M, H, scale=0.1)
 
 
+def layer64(q, ids, keep, renorm):
+    """The layer in FP64 with these choices and this dropout factor."""
+    h = norm64(q["x"], q["w_in"])
+    chosen = torch.softmax(h @ q["w_router"].T, 1).gather(1, ids)
+    probs = chosen / chosen.sum(1, keepdim=True) if renorm else chosen
+    y = 0
+    for j in range(ids.shape[1]):
+        e = ids[:, j]
+        g, u = (torch.einsum("mih,mh->mi", q[n][e], h) for n in ("w_gate", "w_up"))
+        y = y + probs[:, j, None] * torch.einsum("mhi,mi->mh", q["w_down"][e], g * torch.sigmoid(g) * u)
+    return q["x"] + keep * y
+
+
+NAMES = {"dx": "x", "dw_in": "w_in", "dw_router": "w_router", "dW_gate": "w_gate", "dW_up": "w_up", "dW_down": "w_down"}
+
+
+@pytest.mark.parametrize("renorm", [True, False])
+def test_gradients_by_differences(renorm):
+    """Each gradient along a random direction against central differences of the FP64 layer.
+    An error of 3% (6% for the router) in the 2-norm is along a normal direction normal
+    itself, of that deviation: 5 deviations.  The differences' own error, 1e-8 of it, is far below."""
+    w, x, dz = make(40, 64, 72, 5, seed=4)
+    rng = torch.tensor([3, 9], device="cuda")
+    block = MoeTrainBlock(**w, top_k=2, p_drop=0.25, renorm=renorm, eps=EPS)
+    _, saved = block.forward(x, rng)
+    grads = block.backward(dz, saved)
+    ids = saved[4].ids.long().cpu()
+    keep = dgf.dropout(torch.ones_like(x), 0.25, rng).double().cpu()
+    q = {n: t.double().cpu() for n, t in {**w, "x": x}.items()}
+    gen = torch.Generator().manual_seed(5)
+    for name, of in NAMES.items():
+        v = torch.randn(q[of].shape, generator=gen, dtype=torch.float64)
+        step = 1e-4
+        up, down = ((dz.double().cpu() * layer64({**q, of: q[of] + s * v}, ids, keep, renorm)).sum() for s in (step, -step))
+        d = grads[name].double().cpu()
+        share = 0.06 if name == "dw_router" else 0.03
+        assert abs((up - down) / (2 * step) - (d * v).sum()) <= 5 * share * d.norm(), name
+
+
 @pytest.mark.parametrize("renorm", [True, False])
 @pytest.mark.parametrize("M,H,I,E,k,p", [(1, 64, 72, 4, 2, 0.0), (37, 128, 200, 6, 2, 0.25), (300, 256, 320, 20, 4, 0.1),
                                          (700, 320, 264, 60, 8, 0.5)])
@@ -49,21 +88,11 @@ def test_training_step(M, H, I, E, k, p, renorm):
     keep = dgf.dropout(torch.ones_like(x), p, rng).double().cpu()  # 0 or 1 / (1 - p)
 
     q = {n: t.double().cpu().requires_grad_() for n, t in {**w, "x": x}.items()}
-    h = norm64(q["x"], q["w_in"])
-    l = h @ q["w_router"].T
-    chosen = torch.softmax(l, 1).gather(1, ids)
-    probs = chosen / chosen.sum(1, keepdim=True) if renorm else chosen
-    y = 0
-    for j in range(k):
-        e = ids[:, j]
-        g, u = (torch.einsum("mih,mh->mi", q[n][e], h) for n in ("w_gate", "w_up"))
-        y = y + probs[:, j, None] * torch.einsum("mhi,mi->mh", q["w_down"][e], g * torch.sigmoid(g) * u)
-    z64 = q["x"] + keep * y
+    z64 = layer64(q, ids, keep, renorm)
     z64.backward(dz.double().cpu())
     assert off(z, z64.detach()) <= 0.03
-    names = {"dx": "x", "dw_in": "w_in", "dw_router": "w_router", "dW_gate": "w_gate", "dW_up": "w_up", "dW_down": "w_down"}
-    assert set(grads) == set(names)
-    for n, of in names.items():
+    assert set(grads) == set(NAMES)
+    for n, of in NAMES.items():
         assert grads[n].shape == q[of].shape
         want = q[of].grad
         if want.norm() == 0:  # one choice of one expert's weight: no gradient to the router

@@ -144,3 +144,17 @@ def test_captured_products_follow_their_inputs():
         want = dgf.ffn_fwd_w4(x, *p)
         torch.cuda.synchronize()
         assert torch.equal(y, want)
+
+
+@pytest.mark.parametrize("dtype", [BF, FH], ids=str)
+@pytest.mark.parametrize("N,K,group", [(1000, 2304, 64), (520, 4099, 128), (12304, 2048, 32), (300, 6400, 128)])
+def test_a_row_does_not_depend_on_the_batch(dtype, N, K, group):
+    """Wide enough that the waves start at different tiles, and every number of row tiles a workgroup."""
+    gen = torch.Generator(device="cuda").manual_seed(N)
+    w = dgf.pack4(rows(gen, N, K, dtype, K ** -0.5), group)
+    gate, up = (dgf.pack4(rows(gen, K, N, dtype, N ** -0.5), group) for _ in range(2))
+    x, h = rows(gen, 130, K, dtype), rows(gen, 130, N, dtype)
+    y, z = dgf.gemm_w4(x, w), dgf.ffn_fwd_w4(h, gate, up, w)
+    for lo, hi in ((0, 1), (7, 9), (20, 36), (40, 57), (60, 92), (66, 130)):
+        assert torch.equal(dgf.gemm_w4(x[lo:hi], w), y[lo:hi]), (lo, hi)
+        assert torch.equal(dgf.ffn_fwd_w4(h[lo:hi], gate, up, w), z[lo:hi]), (lo, hi)
