@@ -5,10 +5,9 @@
 // A weight is read once for every 32 tokens, so the codes' bytes are the bound: 4.25 bits a
 // weight with groups of 64.  They are laid out so that a wave reads a tile of 16 rows x 128
 // columns as 1 KB in one piece and has each lane's dwords as it feeds them to the matrix core:
-// two operations turn two codes into two operands 24 + c (the code's bits under the leading
-// one of 16.0), and -24 times the sum of the group's activations, from one more product that
-// all rows share, takes the excess out before the scale.  The group's sum, the scaled sums and
-// those over the waves that share K are FP32.
+// c itself as an FP16 operand, c / 16 as a BF16 one, both exact, so that a code of 0 adds
+// nothing however large its activation is, and an infinite activation stays what it is in the
+// formula.  The group's sum, the scaled sums and those over the waves that share K are FP32.
 // Measured at 4096 x 12288, groups of 64, BF16: gate/up 12.4 us for one token (53 MB, 4.3 TB/s),
 // 16.4 for 32; down 11.5 and 17.6.  What is left over the copy rate (10 and 5 us) is one start-up
 // of loads and one reduction a workgroup, and past 16 tokens the activations: each of the down
@@ -108,25 +107,33 @@ __global__ __launch_bounds__(256) void k_unpack4(W4Mat m, uint16_t *w, int64_t l
 
 // ---------------------------------------------------------------- products
 
-// Eight codes as an MFMA operand, each as 16 + code (= 24 + c for the signed c):
-// the code's four bits go under the leading one of 16.0.
+// Eight codes as an MFMA operand, each c / code_unit, exact.
+//  FP16: the code's four bits under the leading one of 16.0 are 24 + c, less 24: three
+//  operations for two codes.
+//  BF16, which has no packed sum: with its highest bit turned, the code is c in four bits of
+//  two's complement, which v_cvt_off_f32_i4 takes from the lowest bits of a byte to c / 16;
+//  the upper halves of two of them are the operands: 14 operations for eight codes.
 template <class T>
 __device__ __forceinline__ typename T::frag code_frag(uint32_t w) {
   uint4 v;
   if constexpr (T::code == 0) {
-    v = make_uint4((w << 3 & 0x00780078u) | 0x41804180u, (w >> 1 & 0x00780078u) | 0x41804180u,
-                   (w >> 5 & 0x00780078u) | 0x41804180u, (w >> 9 & 0x00780078u) | 0x41804180u);
+    const uint32_t even = w ^ 0x88888888u;
+    uint32_t odd = even >> 4;
+    asm("" : "+v"(odd));  // (else each of its bytes gets a shift of its own; bytes are free to pick)
+    auto pair = [](uint32_t u, int lo, int hi) {  // the codes at bits lo and hi
+      return __builtin_amdgcn_perm(__float_as_uint(__builtin_amdgcn_cvt_off_f32_i4((int)(u >> hi & 0xff))),
+                                   __float_as_uint(__builtin_amdgcn_cvt_off_f32_i4((int)(u >> lo & 0xff))), 0x07060302u);
+    };
+    v = make_uint4(pair(even, 0, 16), pair(odd, 0, 16), pair(even, 8, 24), pair(odd, 8, 24));
   } else {
-    v = make_uint4((w << 6 & 0x03c003c0u) | 0x4c004c00u, (w << 2 & 0x03c003c0u) | 0x4c004c00u,
-                   (w >> 2 & 0x03c003c0u) | 0x4c004c00u, (w >> 6 & 0x03c003c0u) | 0x4c004c00u);
+    const f16x2 bias = {(_Float16)24.0f, (_Float16)24.0f};
+    auto pair = [&](uint32_t u) { return __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, (u & 0x03c003c0u) | 0x4c004c00u) - bias); };
+    v = make_uint4(pair(w << 6), pair(w << 2), pair(w >> 2), pair(w >> 6));
   }
   return __builtin_bit_cast(typename T::frag, v);
 }
 template <class T>
-__device__ __forceinline__ typename T::frag bias_frag() {  // -24 throughout
-  const uint32_t b = T::code == 0 ? 0xc1c0c1c0u : 0xce00ce00u;
-  return __builtin_bit_cast(typename T::frag, make_uint4(b, b, b, b));
-}
+constexpr float code_unit = T::code == 0 ? 16.0f : 1.0f;
 
 // Place of the activation (token m, column c, part xp) between the FFN's two kernels: in the
 // order of the down product's fragments, so that each load takes 1 KB in one piece (row by row, rows of 24 KB all start on one L2
@@ -238,29 +245,18 @@ __global__ __launch_bounds__(64 * kW4Waves) void k_w4(W4Params p) {
           }
         }
   };
-  const typename X::frag bias = bias_frag<X>();
   // Half h of a tile.  (A group of 128 columns is scaled in two halves.)
   auto multiply = [&](const Codes &c, const Acts &x, int h) {
     constexpr int kPer = GS == 4 ? 1 : 2;  // 32-column parts with one scale
 #pragma unroll
     for (int q = 0; q < 2; q += kPer) {
-      // -24 times the sum of their activations, from which every row's product starts
-      f32x4 c0[MT];
-#pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        c0[m] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int i = q; i < q + kPer; ++i)
-#pragma unroll
-          for (int xp = 0; xp < XP; ++xp) c0[m] = X::mfma(__builtin_bit_cast(typename X::frag, x.v[xp][m][i]), bias, c0[m]);
-      }
 #pragma unroll
       for (int w = 0; w < W; ++w)
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           f32x4 part[MT];
 #pragma unroll
-          for (int m = 0; m < MT; ++m) part[m] = c0[m];
+          for (int m = 0; m < MT; ++m) part[m] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int i = q; i < q + kPer; ++i) {
             const uint4 &v = c.q[w][n];
@@ -331,6 +327,7 @@ __global__ __launch_bounds__(64 * kW4Waves) void k_w4(W4Params p) {
       v[w] = 0.0f;
 #pragma unroll
       for (int z = 0; z < kW4Waves; ++z) v[w] += red[(z * kOut * 4 + w * NT * MT * 4 + o) * 64 + lane];
+      v[w] *= code_unit<X>;
     }
     const int e = o & 3, m = (o >> 2) % MT, n = (o >> 2) / MT;
     const int64_t row = m0 + 16 * m + 4 * g + e;

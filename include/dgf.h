@@ -450,8 +450,10 @@ dgf_status dgf_unpack4(const void *codes, const void *scales, void *w, int64_t l
  * (W_up x)) with all three.  Made for a few tokens: the weights are read once for
  * every 32.  Sums are FP32 in an order that does not depend on M; y is rounded
  * once; the activation passes between the FFN's two kernels to 2^-16 of its value.
- * Inputs, and the FFN's activations, are finite and below 2^110 (a group's sum
- * passes through 24 times the sum of its inputs).  M <= 65536.  Workspace: dgf_ffn_fwd_w4_workspace bytes.
+ * A code enters its product as it is: one of 0 adds nothing from a finite input, however large, and an
+ * infinite input gives an infinity, or a NaN where the code is 0.  (A group's sum is FP32 before its
+ * scale, so finite inputs from 2^122 on may overflow there.)  M <= 65536.  Workspace:
+ * dgf_ffn_fwd_w4_workspace bytes.
  */
 dgf_status dgf_gemm_w4(const void *x, int64_t ldx, const void *codes, const void *scales, void *y, int64_t ldy, int64_t M,
                        int64_t N, int64_t K, int64_t group, int dtype, void *stream);
