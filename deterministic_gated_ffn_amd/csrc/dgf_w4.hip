@@ -8,11 +8,14 @@
 // c itself as an FP16 operand, c / 16 as a BF16 one, both exact, so that a code of 0 adds
 // nothing however large its activation is, and an infinite activation stays what it is in the
 // formula.  The group's sum, the scaled sums and those over the waves that share K are FP32.
-// Measured at 4096 x 12288, groups of 64, BF16: gate/up 12.4 us for one token (53 MB, 4.3 TB/s),
-// 16.4 for 32; down 11.5 and 17.6.  What is left over the copy rate (10 and 5 us) is one start-up
-// of loads and one reduction a workgroup, and past 16 tokens the activations: each of the down
-// product's 256 workgroups reads all 1.5 MB of them from L2, 400 MB.  (Four workgroups that share
-// K and four times the rows, with a launch that adds them: 22 us.)
+// The activations pass from gate/up to down in three BF16 parts, which add up to the FP32 value:
+// 30 of 131072 outputs then round otherwise than the exact sum does, against 180 of a product
+// in FP32 and 330 with two parts, 17 bits (12288 activations, 32 tokens).
+// Measured at 4096 x 12288, groups of 64, BF16, medians: gate/up 14.0 us for one token (53 MB,
+// 3.8 TB/s), 19.6 for 32; down 12.4 and 27.5.  What is left over the copy rate (10 and 5 us) is one
+// start-up of loads and one reduction a workgroup, and past 16 tokens the activations: each of the
+// down product's 256 workgroups reads all 2.4 MB of them from L2, 600 MB (two parts: 20.8 us; two
+// row tiles a workgroup, on half the CUs: 32).
 #include "dgf_experts.hpp"
 #include "dgf_rows.hpp"
 
@@ -135,19 +138,31 @@ __device__ __forceinline__ typename T::frag code_frag(uint32_t w) {
 template <class T>
 constexpr float code_unit = T::code == 0 ? 16.0f : 1.0f;
 
-// Place of the activation (token m, column c, part xp) between the FFN's two kernels: in the
-// order of the down product's fragments, so that each load takes 1 KB in one piece (row by row, rows of 24 KB all start on one L2
-// channel: the down product took 46 us against 18 at 32 tokens).
-__host__ __device__ inline int64_t act_place(int64_t m, int c, int xp, int64_t tiles_m) {
-  const int64_t piece = ((int64_t)(c / kW4K * 2 + xp) * tiles_m + m / 16) * 4 + c % kW4K / 32;
-  return piece * 512 + ((m & 15) + 16 * (c % 32 / 8)) * 8 + c % 8;
+// An activation passes between the FFN's two kernels as kParts BF16 values whose sum it is.
+constexpr int kParts = 3;
+
+// Place of part xp of the activation (token m, column c): in the order of the down product's
+// fragments, so that each load takes its tokens' lines whole (row by row, rows of 24 KB all start
+// on one L2 channel: the down product took 46 us against 18 at 32 tokens).  Pieces of 8 tokens x
+// 32 columns, the tokens' fastest: a few tokens take half of what a fragment holds.
+__host__ __device__ inline int64_t act_octets(int64_t M) { return (M + 7) / 8; }
+__host__ __device__ inline int64_t act_place(int64_t m, int c, int xp, int64_t octets) {
+  const int64_t piece = ((int64_t)(c / kW4K * kParts + xp) * 4 + c % kW4K / 32) * octets + m / 8;
+  return piece * 256 + ((m & 7) + 8 * (c % 32 / 8)) * 8 + c % 8;
 }
 
-// The activation a of a gate/up pair, as two BF16 values whose sum is a to 2^-17.
-__device__ __forceinline__ void split2(float a, uint16_t &hi, uint16_t &lo) {
-  hi = f2bf(a);
-  const float h = bf2f(hi);
-  lo = h - h == 0.0f ? f2bf(a - h) : 0;
+// The activation a of a gate/up pair in parts: its upper 8 bits, the next 8 and the last 8, cut
+// off, so that each remainder is exact and so is the sum (but for what lies below BF16's
+// smallest subnormal).  An infinity or NaN is its first part.
+__device__ __forceinline__ void split(float a, uint16_t (&part)[kParts]) {
+  const bool finite = a - a == 0.0f;
+  float rest = finite ? a : 0.0f;
+#pragma unroll
+  for (int i = 0; i < kParts; ++i) {
+    part[i] = (uint16_t)(__float_as_uint(rest) >> 16);
+    rest -= bf2f(part[i]);
+  }
+  if (!finite) part[0] = f2bf(a);
 }
 
 __device__ const uint4 kZeros[1] = {};
@@ -173,7 +188,7 @@ struct Scales<S, 4> {
 
 // X: the activations' MFMA type.  S: the scales' (and the output's) type.  MT tiles of 16
 // tokens, NT row tiles of the weights a workgroup (PAIR: NT of gate and NT of up), XP parts
-// the activations come in (2: as act_place puts them), GS groups a tile, TAIL: K is no
+// the activations come in (kParts: as act_place puts them), GS groups a tile, TAIL: K is no
 // multiple of 8, kW4Waves share K: wave z takes the tiles [z n / kW4Waves, (z + 1) n / kW4Waves) of
 // each row, from one that goes by the row tiles: workgroups in step do not all read the same
 // columns of x, which lie on one L2 channel.
@@ -182,10 +197,11 @@ __global__ __launch_bounds__(64 * kW4Waves) void k_w4(W4Params p) {
   constexpr int W = PAIR ? 2 : 1;
   // Tiles in a ring of registers: each is loaded anew as soon as it has been used, so that all
   // but one are on their way.  At 4096 x 12288 against activations one tile ahead and codes two
-  // or four: gate/up 12.4 us against 14.4 for one token and 16.4 against 23.1 for 32, down 11.5
-  // against 12.1 and 17.6 against 19.7.  (Gate/up, one token, 4: 15.5 us, fewer waves fit.
-  // TAIL's loads take more registers.)
-  constexpr int R = MT > 1 ? (TAIL ? 1 : 2) : PAIR || TAIL ? 2 : 4;
+  // or four: gate/up 12.4 us against 14.4 for one token and 16.4 against 23.1 for 32.  (Gate/up,
+  // one token, 4: 15.5 us, fewer waves fit.  TAIL's loads take more registers, and activations in
+  // parts too: the whole FFN takes 24.3 us with two tiles of down in flight, 25.3 with four, and at
+  // 32 tokens 42.3 with one, 42.2 with two.)
+  constexpr int R = XP > 1 ? (MT > 1 ? 1 : 2) : MT > 1 ? (TAIL ? 1 : 2) : PAIR || TAIL ? 2 : 4;
   extern __shared__ __attribute__((aligned(16))) float red[];  // [waves][W NT MT][4][64]
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int i16 = lane & 15, g = lane >> 4;
@@ -235,9 +251,9 @@ __global__ __launch_bounds__(64 * kW4Waves) void k_w4(W4Params p) {
         for (int i = 0; i < 2; ++i) {
           const int64_t row = m0 + 16 * m + i16;
           const int k = kt * kW4K + 64 * h + 32 * i + 8 * g;
-          if constexpr (XP == 2) {  // (a token tile past the last: the last again)
-            const int64_t tiles_m = (p.M + 15) / 16, mt = m0 / 16 + m < tiles_m ? m0 / 16 + m : tiles_m - 1;
-            x.v[xp][m][i] = *reinterpret_cast<const uint4 *>(p.x + (((int64_t)(kt * 2 + xp) * tiles_m + mt) * 4 + 2 * h + i) * 512 + lane * 8);
+          if constexpr (XP > 1) {  // (tokens past the last piece: that one again)
+            const int64_t octets = act_octets(p.M), o = row / 8 < octets ? row / 8 : octets - 1;
+            x.v[xp][m][i] = *reinterpret_cast<const uint4 *>(p.x + ((((int64_t)kt * kParts + xp) * 4 + 2 * h + i) * octets + o) * 256 + ((i16 & 7) + 8 * g) * 8);
           } else if constexpr (TAIL) {
             x.v[xp][m][i] = row < p.M && k < p.K ? row_ld(p.x + row * p.ldx, k, p.K) : make_uint4(0, 0, 0, 0);
           } else {
@@ -334,15 +350,19 @@ __global__ __launch_bounds__(64 * kW4Waves) void k_w4(W4Params p) {
     const int col = (nt0 + n) * kW4Rows + i16;
     if (row >= p.M || (!PAIR && col >= p.N)) continue;
     if constexpr (PAIR) {
-      const int64_t tiles_m = (p.M + 15) / 16;
+      const int64_t octets = act_octets(p.M);
       if (nt0 + n < tiles_n) {
         const float sg = 1.0f / (1.0f + expf(-v[0]));
-        split2(col < p.N ? v[0] * sg * v[1] : 0.0f, p.y[act_place(row, col, 0, tiles_m)], p.y[act_place(row, col, 1, tiles_m)]);
+        uint16_t part[kParts];
+        split(col < p.N ? v[0] * sg * v[1] : 0.0f, part);
+#pragma unroll
+        for (int xp = 0; xp < kParts; ++xp) p.y[act_place(row, col, xp, octets)] = part[xp];
       }
       // the columns that fill up the last tile of the down product are zeros
       if (nt0 + n == tiles_n - 1)
         for (int c = col + kW4Rows; c < (tiles_n * kW4Rows + kW4K - 1) / kW4K * kW4K; c += kW4Rows)
-          p.y[act_place(row, c, 0, tiles_m)] = p.y[act_place(row, c, 1, tiles_m)] = 0;
+#pragma unroll
+          for (int xp = 0; xp < kParts; ++xp) p.y[act_place(row, c, xp, octets)] = 0;
     } else {
       p.y[row * p.ldy + col] = S::r(v[0]);
     }
@@ -366,7 +386,7 @@ hipError_t w4_launch(const W4Params &p, hipStream_t s) {
 
 template <class X, class S, int MT, bool DOWN, bool PAIR, int GS>
 hipError_t w4_n(const W4Params &p, hipStream_t s) {
-  constexpr int XP = DOWN ? 2 : 1;
+  constexpr int XP = DOWN ? kParts : 1;
   // Up to 16 tokens one row tile a workgroup (gate/up 12288 x 4096, one token, with less in
   // flight than now: 14.3 us, two tiles 18.1, three 15.6).  Past that as many as make the least
   // of what its waves read of the weights and, from L2, of the activations, over the rounds of
@@ -383,7 +403,7 @@ hipError_t w4_n(const W4Params &p, hipStream_t s) {
   }
   return w4_launch<X, S, MT, 1, XP, PAIR, GS>(p, s);
 }
-// DOWN: the FFN's second product, whose activations are in two parts.
+// DOWN: the FFN's second product, whose activations are in parts.
 template <class X, class S, bool DOWN, bool PAIR, int GS>
 hipError_t w4_m(const W4Params &p, hipStream_t s) {
   return p.M <= 16 ? w4_n<X, S, 1, DOWN, PAIR, GS>(p, s) : w4_n<X, S, 2, DOWN, PAIR, GS>(p, s);
@@ -415,7 +435,8 @@ hipError_t launch_unpack4(W4Mat m, uint16_t *w, int64_t ldw, int N, int K, int g
   return hipGetLastError();
 }
 
-size_t w4_act_bytes(int64_t M, int I) { return (size_t)w4_tiles_k(I) * 2 * ((M + 15) / 16) * 4 * 1024; }
+// (in whole pages of 4 KB)
+size_t w4_act_bytes(int64_t M, int I) { return ((size_t)w4_tiles_k(I) * kParts * 4 * act_octets(M) * 512 + 4095) / 4096 * 4096; }
 
 hipError_t launch_w4(const W4Params &p, hipStream_t s) {
   return p.fmt == FMT_F16 ? w4_g<F16, F16, false, false>(p, s) : w4_g<Bf16, Bf16, false, false>(p, s);

@@ -449,7 +449,7 @@ dgf_status dgf_unpack4(const void *codes, const void *scales, void *w, int64_t l
  * y [M,N] = x [M,K] w^T with w in 4 bits, and the FFN y = W_down (silu(W_gate x)
  * (W_up x)) with all three.  Made for a few tokens: the weights are read once for
  * every 32.  Sums are FP32 in an order that does not depend on M; y is rounded
- * once; the activation passes between the FFN's two kernels to 2^-16 of its value.
+ * once; the activation passes between the FFN's two kernels in FP32.
  * A code enters its product as it is: one of 0 adds nothing from a finite input, however large, and an
  * infinite input gives an infinity, or a NaN where the code is 0.  (A group's sum is FP32 before its
  * scale, so finite inputs from 2^122 on may overflow there.)  M <= 65536.  Workspace:

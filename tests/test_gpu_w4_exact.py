@@ -109,3 +109,56 @@ def test_ffn(dtype, group, M, H, I):
     assert (a.abs() @ cd.abs().T).max() < BITS
     y = dgf.ffn_fwd_w4(matrix(x, dtype), packed(cg, 1.0, dtype, group), packed(cu, 0.25, dtype, group), packed(cd, 2.0 ** -10, dtype, group))
     assert torch.equal(y.cpu(), once(a @ cd.T * 2.0 ** -12, dtype))
+
+
+@pytest.mark.parametrize("dtype", [BF, FH], ids=str)
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("M", [1, 9, 18, 40])
+def test_activations_pass_whole(dtype, group, M):
+    """Activations of 20 bits, of which the second product takes differences of a few units: every bit counts."""
+    gen = torch.Generator().manual_seed(M)
+    H, I = 40, 300
+    digits = torch.randint(0, 8, (I, 6), generator=gen)  # of u, base 8
+    digits[1::2, 1:] = digits[::2, 1:]                   # pairs that differ in the last one
+    digits[::32] = 0                                     # the columns of the second product that hold a group's 7
+    cg, cu, cd = torch.zeros(I, H).double(), torch.zeros(I, H).double(), torch.zeros(H, I).double()
+    cg[:, ::group] = cu[:, ::group] = cd[:, ::group] = 7.0
+    cg[:, 7], cu[:, 1:7] = 6.0, digits.double()
+    for n in range(H):
+        i = 2 * n + 2 + 128 * (n % 2)
+        cd[n, i], cd[n, i + 1] = (1.0, -1.0) if i % 32 else (0.0, 0.0)
+    x = torch.zeros(M, H).double()
+    x[:, 1:7] = 8.0 ** torch.arange(6) * torch.tensor([1.0, -1.0, 0.5, -0.25, 0.125])[torch.arange(M) % 5, None]
+    x[:, 7] = 4.0  # g = 24
+    a = 24.0 * (x @ cu.T)
+    y = dgf.ffn_fwd_w4(matrix(x, dtype), packed(cg, 1.0, dtype, group), packed(cu, 1.0, dtype, group), packed(cd, 2.0 ** -4, dtype, group))
+    assert torch.equal(y.cpu(), once(a @ cd.T * 2.0 ** -4, dtype))
+
+
+@pytest.mark.parametrize("dtype", [BF, FH], ids=str)
+@pytest.mark.parametrize("M", [1, 20])
+def test_infinite_activations_pass(dtype, M):
+    """An infinite activation is an infinity in the second product too, and only its token's."""
+    H, I, group = 40, 72, 32
+    cg, cu, cd = torch.zeros(I, H).double(), torch.zeros(I, H).double(), torch.zeros(H, I).double()
+    cg[:, ::group] = cu[:, ::group] = cd[:, ::group] = 7.0
+    cg[5, 3], cg[6, 4] = 7.0, 1.0
+    cu[5, 3], cu[6, 4] = -7.0, 2.0
+    cd[:30, 5] = torch.arange(30).double() % 8 - 4
+    cd[:, 6] = 3.0
+    x = torch.zeros(M, H).double()
+    x[:, 4] = 32.0
+    x[M // 2, 3] = inf
+    y = dgf.ffn_fwd_w4(matrix(x, dtype), *(packed(c, 1.0, dtype, group) for c in (cg, cu, cd)))
+    a = torch.zeros(M, I).double()
+    a[:, 6] = 32.0 * 64.0
+    want = a @ cd.T
+    # every other row of gate and up has a code of 0 there: 0 times infinity
+    want[M // 2] = nan
+    assert torch.equal(y.cpu().nan_to_num(nan=12345.0), once(want, dtype).nan_to_num(nan=12345.0))
+    if dtype == BF:  # finite inputs whose activation overflows
+        x[M // 2, 3] = 2.0 ** 70
+        y = dgf.ffn_fwd_w4(matrix(x, dtype), *(packed(c, 1.0, dtype, group) for c in (cg, cu, cd)))
+        want = a @ cd.T
+        want[M // 2] = torch.where(cd[:, 5] == 0, nan, torch.where(cd[:, 5] > 0, -inf, inf))
+        assert torch.equal(y.cpu().nan_to_num(nan=12345.0), once(want, dtype).nan_to_num(nan=12345.0))
