@@ -369,12 +369,17 @@ __global__ __launch_bounds__(64 * kW4Waves) void k_w4(W4Params p) {
   }
 }
 
+// Row tiles a workgroup may take.  (Three pairs with ragged rows and groups of 32 need more
+// registers than there are: with 100 of them spilled the FFN took 92 us at 32 tokens, 4099 x
+// 12288, against 76 with two, but 28 against 31 at 1003 x 8200.)
+constexpr int w4_most(int MT, bool PAIR, int GS, bool tail) { return MT == 1 ? 1 : PAIR && GS == 4 && tail ? 2 : 3; }
+
 template <class X, class S, int MT, int NT, int XP, bool PAIR, int GS>
 hipError_t w4_launch(const W4Params &p, hipStream_t s) {
   const int tiles_n = (p.N + kW4Rows - 1) / kW4Rows;
   const dim3 g((tiles_n + NT - 1) / NT, (uint32_t)((p.M + 16 * MT - 1) / (16 * MT))), b(64 * kW4Waves);
   const size_t lds = (size_t)kW4Waves * (PAIR ? 2 : 1) * NT * MT * 4 * 64 * 4;
-  if constexpr (XP == 1) {
+  if constexpr (XP == 1 && NT <= w4_most(MT, PAIR, GS, true)) {
     if (p.K % 8) {
       dgf_launch((k_w4<X, S, MT, NT, XP, PAIR, GS, true>), g, b, lds, s, p);
       return hipGetLastError();
@@ -393,7 +398,7 @@ hipError_t w4_n(const W4Params &p, hipStream_t s) {
   // workgroups (32 tokens, likewise: 31.5 us, 26.7, 23.2).
   const int tiles = (p.N + kW4Rows - 1) / kW4Rows;
   int best = 1, cost = 0;
-  for (int n = 1; n <= (MT > 1 ? 3 : 1); ++n) {
+  for (int n = 1; n <= w4_most(MT, PAIR, GS, !DOWN && p.K % 8); ++n) {
     const int c = (tiles + 256 * n - 1) / (256 * n) * ((PAIR ? 2 : 1) * n + XP * MT);
     if (n == 1 || c < cost) best = n, cost = c;
   }
