@@ -98,8 +98,11 @@ dgf_status dgf_gemm_grouped(int layout, const void *A, int64_t lda, const void *
   // workgroups of the smallest tile
   const int64_t cols = (N + 127) / 128, tiles = tn ? (M + 127) / 128 * cols * E : (R / 64 + (R < E ? R : E)) * cols;
   if (tiles > INT32_MAX) return fail(DGF_EUNSUPPORTED, "grouped products: more than 2^31 output tiles");
-  if ((A2 == nullptr) != (B2 == nullptr)) return fail(DGF_EINVAL, "A2 and B2 must both be given or both be NULL");
-  if (tn && A2) return fail(DGF_EINVAL, "DGF_TN takes one pair of operands");
+  const bool two = A2 || B2;
+  // (a matrix without rows or columns may be NULL)
+  if (two && (!A2 || !B2) && (tn || (K > 0 && (rows ? T : R) > 0 && N > 0)))
+    return fail(DGF_EINVAL, "A2 and B2 must both be given or both be NULL");
+  if (tn && two) return fail(DGF_EINVAL, "DGF_TN takes one pair of operands");
   if (rows && T < 0) return fail(DGF_EINVAL, "T=%lld rows to choose from", (long long)T);
   if (rows && T > kMaxRows) return fail(DGF_EUNSUPPORTED, "T=%lld beyond the limit (2^25 rows)", (long long)T);
   if (M == 0 || N == 0) return ok();
@@ -114,7 +117,7 @@ dgf_status dgf_gemm_grouped(int layout, const void *A, int64_t lda, const void *
     const int64_t b_rows = layout == DGF_NT ? N : K, b_cols = layout == DGF_NT ? K : N;
     DGF_TRY(check_mat("A", A, lda, listed, K));
     if (K > 0) DGF_TRY(check_experts("B", B, ldb, stride_b, E, b_rows, b_cols));
-    if (A2) {
+    if (two) {
       DGF_TRY(check_mat("A2", A2, lda2, listed, K));
       if (K > 0) DGF_TRY(check_experts("B2", B2, ldb2, stride_b2, E, b_rows, b_cols));
     }
@@ -123,7 +126,7 @@ dgf_status dgf_gemm_grouped(int layout, const void *A, int64_t lda, const void *
   GroupedParams p{};
   p.t[0] = GroupedTerm{(const uint16_t *)A, (const uint16_t *)B, lda, ldb, stride_b};
   p.t[1] = GroupedTerm{(const uint16_t *)A2, (const uint16_t *)B2, lda2, ldb2, stride_b2};
-  p.terms = A2 ? 2 : 1;
+  p.terms = two ? 2 : 1;
   p.rows = rows;
   p.T = listed;
   p.off = offsets;
