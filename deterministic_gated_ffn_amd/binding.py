@@ -69,6 +69,7 @@ SIGNATURES = {
     "dgf_moe_fwd_workspace": (_SZ, [_I64, _I64, _I64, _I64, _I64, _I64]),
     "dgf_moe_fwd": (_I, [_P, _I64, _P, _I64, _P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _P, _I64, _P, _P,
                          _I64, _I64, _I64, _I64, _I64, _I64, _I64, _I, _P, _SZ, _I, _P]),
+    "dgf_moe_logits": (_I, [_P, _I64, _P, _I64, _P, _I64, _I64, _I64, _I64, _I, _P]),
     "dgf_moe_route_workspace": (_SZ, [_I64, _I64, _I64]),
     "dgf_moe_route": (_I, [_P, _I64, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I, _P, _SZ, _I, _P]),
     "dgf_moe_route_bwd": (_I, [_P, _P, _I64, _P, _P, _P, _I64, _I64, _I64, _I64, _I, _I, _P]),
@@ -704,6 +705,20 @@ def _logits(t: torch.Tensor, name: str):
     if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
         raise ValueError(f"{name}: expected a 2-D row-major view (stride(1) == 1)")
     return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t.shape[1], _LOGITS[t.dtype]
+
+
+def moe_logits(x, w_router, stream=None):
+    """The router's logits x w_router^T in float32 [M, E] (dgf_moe_logits)."""
+    L = load()
+    dt = _stored(x)
+    xp, ldx = _mat(x, "x")
+    (M, H), E = x.shape, w_router.shape[0]
+    with _on(stream):
+        _here(x, "x")
+        wr, ldr = _rows(w_router, (E, H), x, "w_router")
+        logits = x.new_empty((M, E), dtype=torch.float32)
+        _check(L.dgf_moe_logits(xp, ldx, wr, ldr, logits.data_ptr(), E, M, H, E, dt, _stream(stream)), "dgf_moe_logits")
+    return logits
 
 
 def moe_route(logits, top_k: int, renorm: bool = True, stream=None) -> MoePlan:

@@ -15,7 +15,7 @@ of 16).  Serving replaces the FFN with moe_fwd, or with ffn_fwd_w4 (weights in
 4 bits).  A mixture of experts is trained as MoeTrainBlock:
 
     h       = norm(x; w_in)                           norm_fwd
-    l       = h w_router^T                            gemm_tree
+    l       = h w_router^T in FP32                    moe_logits
     plan    = k experts a token, rows by expert       moe_route
     g, u    = h W_gate,e^T, h W_up,e^T                gemm_grouped (rows of h by the plan's list)
     o       = silu(g) u W_down,e^T                    act_fwd, gemm_grouped
@@ -24,6 +24,8 @@ of 16).  Serving replaces the FFN with moe_fwd, or with ffn_fwd_w4 (weights in
     python -m deterministic_gated_ffn_amd.block       # training steps and served batches
 """
 from __future__ import annotations
+
+import contextlib
 
 import torch
 
@@ -91,6 +93,13 @@ class FfnBlock4:
         return dgf.norm_fwd(x, y, w_post=self.w_out, gate=self.gate, alpha=self.alpha, eps=self.eps, stream=stream)["z"]
 
 
+def _stored(t, like, stream):
+    """A float32 matrix rounded once to like's type, in rows that the products take."""
+    with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
+        rows, cols = t.shape
+        return like.new_empty((rows, (cols + 7) // 8 * 8))[:, :cols].copy_(t)
+
+
 class MoeTrainBlock:
     """z = x + dropout(MoE(norm(x))) over any number of tokens, forward and backward.
     I and H are multiples of 8; a token whose logits are all -inf goes nowhere."""
@@ -105,7 +114,7 @@ class MoeTrainBlock:
         to be as it is now when the backward runs."""
         pre = dgf.norm_fwd(x, w_next=self.w_in, eps=self.eps, training=True, stream=stream)
         h = pre["h"]
-        logits = dgf.gemm_tree("NT", h, self.w_router, stream=stream)
+        logits = dgf.moe_logits(h, self.w_router, stream=stream)
         plan = dgf.moe_route(logits, self.top_k, renorm=self.renorm, stream=stream)
         g = dgf.gemm_grouped("NT", h, self.w_gate, plan.offsets, rows=plan.rows, stream=stream)
         u = dgf.gemm_grouped("NT", h, self.w_up, plan.offsets, rows=plan.rows, stream=stream)
@@ -126,7 +135,7 @@ class MoeTrainBlock:
         # the gate and up lanes of a row in one sum, then the rows of a token
         dh = dgf.moe_combine(dgf.gemm_grouped("NN", dg, self.w_gate, off, add=(du, self.w_up), stream=stream), plan.pos,
                              stream=stream)
-        dlogits = dgf.moe_route_bwd(dprobs, logits, plan.ids, plan.probs, renorm=self.renorm, stream=stream)
+        dlogits = _stored(dgf.moe_route_bwd(dprobs, logits, plan.ids, plan.probs, renorm=self.renorm, stream=stream), x, stream)
         # (p = 0 keeps everything: the router's share of dh added to the experts')
         dh = dgf.dropout(dgf.gemm_tree("NN", dlogits, self.w_router, stream=stream), 0.0, rng, res=dh, stream=stream)
         pre = dgf.norm_bwd(dz, dh, x, w_next=self.w_in, rstd=rstd, stream=stream)

@@ -21,7 +21,7 @@ struct GroupedParams {
   int terms;            // 2: NN and NT only
   const int *rows;      // [R] or null: r itself
   int64_t T;            // rows of the operand that `rows` points into (R without it)
-  const int *off;       // [E + 1]
+  const int *off;       // [E + 1]; null: one expert has all rows
   uint16_t *C;
   int64_t ldc, stride_c;
   int64_t R;
@@ -30,6 +30,8 @@ struct GroupedParams {
   int tiles_m, tiles_n;  // of one expert's matrix (NT, NN: columns only), set by the launch
 };
 hipError_t launch_grouped(const GroupedParams &p, hipStream_t s);
+// One NT product of all rows (no offsets, one expert) whose sums are stored in FP32: C and ldc are of floats.
+hipError_t launch_router(const GroupedParams &p, hipStream_t s);
 
 // Routing (dgf_route.hip): each token's k largest logits, their weights, and
 // the (token, choice) pairs sorted by expert.

@@ -139,6 +139,31 @@ dgf_status dgf_gemm_grouped(int layout, const void *A, int64_t lda, const void *
   return ok();
 }
 
+dgf_status dgf_moe_logits(const void *x, int64_t ldx, const void *w_router, int64_t ld_wr, float *logits, int64_t ld, int64_t M,
+                          int64_t H, int64_t E, int dtype, void *stream) {
+  int fmt = 0;
+  DGF_TRY(stored_type(dtype, &fmt));
+  if (M < 0 || H < 0) return fail(DGF_EINVAL, "negative dimension (M=%lld H=%lld)", (long long)M, (long long)H);
+  if (E < 1) return fail(DGF_EINVAL, "E=%lld experts: need at least 1", (long long)E);
+  if (M > kMaxTokens || E > kExpertsMaxE || H >= kMaxLd)
+    return fail(DGF_EUNSUPPORTED, "router: M <= 2^21, E <= %d, H below 2^23 (M=%lld H=%lld E=%lld)", kExpertsMaxE, (long long)M,
+                (long long)H, (long long)E);
+  if (M == 0) return ok();
+  DGF_TRY(check_mat("x", x, ldx, M, H));
+  DGF_TRY(check_mat("w_router", w_router, ld_wr, E, H));
+  DGF_TRY(check_logits("logits", logits, ld, DGF_FP32, M, E));
+  GroupedParams p{};
+  p.t[0] = GroupedTerm{(const uint16_t *)x, (const uint16_t *)w_router, ldx, ld_wr, 0};
+  p.terms = 1;
+  p.T = p.R = M;
+  p.C = reinterpret_cast<uint16_t *>(logits); p.ldc = ld;
+  p.N = (int)E; p.K = (int)H; p.E = 1;
+  p.layout = DGF_NT; p.fmt = fmt;
+  hipStream_t s = (hipStream_t)stream;
+  DGF_TRY(hip_check(timed(s, "router", [&] { return launch_router(p, s); }), "router"));
+  return ok();
+}
+
 size_t dgf_moe_route_workspace(int64_t M, int64_t E, int64_t k) {
   if (M <= route_once() || M > kMaxTokens || E < 1 || E > kExpertsMaxE || k < 1 || k > kExpertsMaxK || k > E) return 0;
   return round256((size_t)route_blocks(M) * E * 2);

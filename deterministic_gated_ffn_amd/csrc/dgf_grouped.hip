@@ -122,7 +122,7 @@ __device__ __forceinline__ void zero_tail(uint16_t *tile, int rows, int kv) {
 // (Read as constants: by the scalar unit, beside the counted vector loads.)
 __device__ __forceinline__ void expert_rows(const GroupedParams &p, int e, int &lo, int &hi) {
   const auto *off = (const __attribute__((address_space(4))) int *)(uintptr_t)p.off;
-  const int R = (int)p.R, l = off[e], h = off[e + 1];
+  const int R = (int)p.R, l = off ? off[e] : 0, h = off ? off[e + 1] : R;
   lo = l < 0 ? 0 : l > R ? R : l;
   hi = h < lo ? lo : h > R ? R : h;
 }
@@ -278,7 +278,8 @@ struct Tiles {
 
 // A workgroup's tiles as one stream of stages: while a stage is multiplied, the loads of
 // the next ones, of this tile or the ones after it, are under way.
-template <class T, int LAYOUT, int WN, int FMAX, int FNMAX, int NS>
+// OUT32: the sums are stored as they are, in FP32 (C, of any alignment, is of floats).
+template <class T, int LAYOUT, int WN, int FMAX, int FNMAX, int NS, bool OUT32>
 struct Stream {
   static constexpr bool ATR = LAYOUT == DGF_LAYOUT_TN, BTR = LAYOUT != DGF_LAYOUT_NT;
   static constexpr int WAVES = 2 * WN, BM = 32 * FMAX, BN = 16 * WN * FNMAX, kStage = (BM + BN) * kU * 2;
@@ -470,6 +471,23 @@ struct Stream {
     return st;
   }
 
+  template <int FM, int FN>
+  __device__ __forceinline__ void store32(const Tile &t, const f32x4 (&acc)[FM][FN]) {
+    const int lane = fresh(this->lane), r0 = t.lo + wm * FM * 16 + (lane & 15), c0 = t.n0 + wn * FN * 16 + 4 * (lane >> 4);
+    float *o = reinterpret_cast<float *>(p.C) + (int64_t)r0 * p.ldc + c0;
+#pragma unroll
+    for (int m = 0; m < FM; ++m) {
+      if (r0 + 16 * m < t.hi) {
+#pragma unroll
+        for (int n = 0; n < FN; ++n)
+#pragma unroll
+          for (int z = 0; z < 4; ++z)
+            if (c0 + 16 * n + z < p.N) o[16 * n + z] = acc[m][n][z];
+      }
+      o += 16 * p.ldc;
+    }
+  }
+
   // Multiplies out tile number n of the run, of 32 FM rows (or fewer) x 64 FN columns, with
   // contraction klen, and stores it.
   template <int FM, int FN>
@@ -529,6 +547,10 @@ struct Stream {
     // row: half the requests (TN, 32768 rows over 128 experts, 768 x 2048: 209 us against
     // 240 with 8-byte stores).
     const Tile t = tiles.get(number);
+    if constexpr (OUT32) {
+      store32<FM, FN>(t, acc);
+      return;
+    }
     const int out_lane = fresh(lane), i = out_lane & 15, q4 = out_lane >> 4;
     const int row0 = ATR ? t.row0 : t.lo, rend = ATR ? p.M : t.hi;
     const int r0 = row0 + wm * FM * 16 + i, c0 = t.n0 + wn * FN * 16;
@@ -611,19 +633,19 @@ struct Stream {
   }
 };
 
-template <class T, int LAYOUT, int WN, int FM, int FN, int NS>
+template <class T, int LAYOUT, int WN, int FM, int FN, int NS, bool OUT32>
 __global__ __launch_bounds__(128 * WN) void k_grouped(GroupedParams p) {
   extern __shared__ __attribute__((aligned(16))) char lds[];
-  Stream<T, LAYOUT, WN, FM, FN, NS> s(p, lds);
+  Stream<T, LAYOUT, WN, FM, FN, NS, OUT32> s(p, lds);
   s.go();
 }
 
-template <class T, int LAYOUT, int WN, int FM, int FN, int NS>
+template <class T, int LAYOUT, int WN, int FM, int FN, int NS, bool OUT32>
 hipError_t grouped_launch(GroupedParams p, int groups, hipStream_t s) {
   constexpr int BM = 32 * FM, BN = 16 * WN * FN;
   p.tiles_m = (p.M + BM - 1) / BM;
   p.tiles_n = (p.N + BN - 1) / BN;
-  dgf_launch((k_grouped<T, LAYOUT, WN, FM, FN, NS>), dim3(groups), dim3(128 * WN), (size_t)NS * (BM + BN) * kU * 2 + Tiles<LAYOUT, BM, BN>::bytes(p.E), s, p);
+  dgf_launch((k_grouped<T, LAYOUT, WN, FM, FN, NS, OUT32>), dim3(groups), dim3(128 * WN), (size_t)NS * (BM + BN) * kU * 2 + Tiles<LAYOUT, BM, BN>::bytes(p.E), s, p);
   return hipGetLastError();
 }
 
@@ -631,16 +653,16 @@ hipError_t grouped_launch(GroupedParams p, int groups, hipStream_t s) {
 // (8192^3: 1268 us against 901); 64 x 128 with more stages in flight where an expert has 64
 // rows or fewer on average, whose products are bound by reading the weights (128 experts of 64
 // rows, 2048 -> 1024: 137 us).
-template <class T, int LAYOUT>
+template <class T, int LAYOUT, bool OUT32 = false>
 hipError_t grouped_l(const GroupedParams &p, hipStream_t s) {
   const int64_t strips = (p.N + 255) / 256;
   if constexpr (LAYOUT == DGF_LAYOUT_TN) {
-    if ((int64_t)((p.M + 255) / 256) * strips * p.E >= 256) return grouped_launch<T, LAYOUT, 4, 8, 4, 4>(p, 256, s);
-    return grouped_launch<T, LAYOUT, 4, 4, 2, 4>(p, 512, s);
+    if ((int64_t)((p.M + 255) / 256) * strips * p.E >= 256) return grouped_launch<T, LAYOUT, 4, 8, 4, 4, OUT32>(p, 256, s);
+    return grouped_launch<T, LAYOUT, 4, 4, 2, 4, OUT32>(p, 512, s);
   } else {
-    if (p.R / p.E <= 64) return grouped_launch<T, LAYOUT, 4, 2, 2, 6>(p, 512, s);
-    if (p.R / 256 * strips >= 192) return grouped_launch<T, LAYOUT, 4, 8, 4, 4>(p, 256, s);
-    return grouped_launch<T, LAYOUT, 4, 4, 2, 4>(p, 512, s);
+    if (p.R / p.E <= 64) return grouped_launch<T, LAYOUT, 4, 2, 2, 6, OUT32>(p, 512, s);
+    if (p.R / 256 * strips >= 192) return grouped_launch<T, LAYOUT, 4, 8, 4, 4, OUT32>(p, 256, s);
+    return grouped_launch<T, LAYOUT, 4, 4, 2, 4, OUT32>(p, 512, s);
   }
 }
 
@@ -654,6 +676,10 @@ hipError_t grouped_t(const GroupedParams &p, hipStream_t s) {
 }
 
 }  // namespace
+
+hipError_t launch_router(const GroupedParams &p, hipStream_t s) {
+  return p.fmt == FMT_F16 ? grouped_l<F16, DGF_LAYOUT_NT, true>(p, s) : grouped_l<Bf16, DGF_LAYOUT_NT, true>(p, s);
+}
 
 hipError_t launch_grouped(const GroupedParams &p, hipStream_t s) {
   return p.fmt == FMT_F16 ? grouped_t<F16>(p, s) : grouped_t<Bf16>(p, s);

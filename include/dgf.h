@@ -353,6 +353,16 @@ dgf_status dgf_moe_fwd(const void *x, int64_t ldx, const void *w_router, int64_t
  */
 
 /*
+ * The router's logits = x w_router^T, [M,E] in FP32 (any ld >= E), from x [M,H] and
+ * w_router [E,H].  Sums are FP32 in one order whatever the other rows are, and not
+ * rounded: a logit's last bits decide which experts a token takes (from logits of
+ * 16 bits some tokens take others).  dgf_moe_fwd sums in another order: the two
+ * choose alike but where logits are equal up to FP32 rounding.
+ */
+dgf_status dgf_moe_logits(const void *x, int64_t ldx, const void *w_router, int64_t ld_wr, float *logits, int64_t ld, int64_t M,
+                          int64_t H, int64_t E, int dtype, void *stream);
+
+/*
  * Routing.  logits [M,E] (dtype BF16, FP16 or FP32; any ld >= E, aligned to
  * its elements).  A token takes its k largest logits in descending order, ties
  * (-0 and +0 are one) to the lowest index; NaN counts as -infinity, +infinity
