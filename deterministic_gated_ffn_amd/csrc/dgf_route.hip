@@ -124,7 +124,6 @@ struct RouteLds {
   int hist[kExpertsMaxE];
   int base[kExpertsMaxE];                 // first sorted row of the block's pairs, by expert
   int wave_sums[kRouteWaves];
-  uint32_t part[kRouteThreads];
   int wave_base[kRouteWaves][kExpertsMaxE];
 };
 
