@@ -404,6 +404,11 @@ dgf_status dgf_moe_route_bwd(const float *dprobs, const void *logits, int64_t ld
  * output is rounded once.  Rows of C outside [offsets[0], offsets[E]) are left as
  * they were; K = 0 and experts without rows (TN) give +0.  Offsets are taken
  * within [0, rows]; an index outside [0, T) reads as a row of zeros.
+ * Rows of A, B, A2 and B2 are read in pieces of 8 elements: up to 7 past a row's last one,
+ * to the next multiple of 8, whatever they hold, also behind a matrix's last row (the
+ * same 16 bytes as its last element, which never end on another page).  The same
+ * holds for dgf_moe_logits.  Nothing is written outside of C's columns.  An empty
+ * matrix may be NULL.
  */
 dgf_status dgf_gemm_grouped(int layout, const void *A, int64_t lda, const void *B, int64_t ldb, int64_t stride_b,
                             const void *A2, int64_t lda2, const void *B2, int64_t ldb2, int64_t stride_b2,
@@ -416,7 +421,7 @@ dgf_status dgf_gemm_grouped(int layout, const void *A, int64_t lda, const void *
  * in FP32, j ascending; choices with pos outside [0, R) add nothing.  Backward:
  *   d_o[pos[m,j]] = probs[m,j] dy[m],  dprobs[m,j] = <dy[m], o[pos[m,j]]>  (0 without a row)
  * dprobs may be NULL (o is not read then).  A row of d_o that no pos names is
- * left as it was; no two pos may name the same row.
+ * left as it was; no two pos may name the same row.  H = 0 with dprobs is DGF_EINVAL.
  */
 dgf_status dgf_moe_combine(const void *o, int64_t ld_o, int64_t R, const int32_t *pos, const float *probs, void *y,
                            int64_t ldy, int64_t M, int64_t H, int64_t k, int dtype, void *stream);
