@@ -395,11 +395,12 @@ hipError_t w4_n(const W4Params &p, hipStream_t s) {
   // Up to 16 tokens one row tile a workgroup (gate/up 12288 x 4096, one token, with less in
   // flight than now: 14.3 us, two tiles 18.1, three 15.6).  Past that as many as make the least
   // of what its waves read of the weights and, from L2, of the activations, over the rounds of
-  // workgroups (32 tokens, likewise: 31.5 us, 26.7, 23.2).
-  const int tiles = (p.N + kW4Rows - 1) / kW4Rows;
-  int best = 1, cost = 0;
+  // workgroups, those of every token tile counted (gate/up, 32 tokens, likewise: 31.5 us, 26.7,
+  // 23.2; the FFN of 4096 x 12288 at 64 tokens with one row tile of down 83.6 us, with two 69.9).
+  const int64_t tiles = (p.N + kW4Rows - 1) / kW4Rows, token_tiles = (p.M + 16 * MT - 1) / (16 * MT);
+  int64_t best = 1, cost = 0;
   for (int n = 1; n <= w4_most(MT, PAIR, GS, !DOWN && p.K % 8); ++n) {
-    const int c = (tiles + 256 * n - 1) / (256 * n) * ((PAIR ? 2 : 1) * n + XP * MT);
+    const int64_t c = ((tiles + n - 1) / n * token_tiles + 255) / 256 * ((PAIR ? 2 : 1) * n + XP * MT);
     if (n == 1 || c < cost) best = n, cost = c;
   }
   if constexpr (MT > 1) {
