@@ -21,7 +21,7 @@ struct GroupedParams {
   int terms;            // 2: NN and NT only
   const int *rows;      // [R] or null: r itself
   int64_t T;            // rows of the operand that `rows` points into (R without it)
-  const int *off;       // [E + 1]; null: one expert has all rows
+  const int *off;       // [E + 1]; not read by launch_router
   uint16_t *C;
   int64_t ldc, stride_c;
   int64_t R;

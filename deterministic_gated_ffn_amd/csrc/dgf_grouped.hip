@@ -10,8 +10,9 @@
 // registers, four of them in 128 KB, so that two are on their way while one is multiplied;
 // one barrier a stage publishes the one that has landed, and the fragments of A are read a
 // few products ahead of their use.  Operands whose contraction runs across rows are read back
-// transposed, four rows at a time.  A row list costs nothing: every lane has its row's
-// address.
+// transposed, four rows at a time.  With a row list every lane has its row's address, which NT and
+// NN look up once a tile (32768 rows over 128 experts, rows in order: 175 us with a list and
+// without) and TN at every stage (213 against 194).
 //
 // The grid is one workgroup a CU (two of the smaller tiles) for the whole call; each takes its
 // share of all tiles as one stream of stages, the next tile's loads under way while the last
@@ -19,12 +20,14 @@
 // Everything that is the same for a whole wave is kept in scalar registers: state that the
 // compiler moved to vector registers cost the accumulators theirs.
 //
-// Measured, BF16: 8192^3 NT / NN / TN 901 / 890 / 990 us (1220 / 1235 / 1111 TFLOP/s; a
-// library's plain product 750).  32768 rows over 128 experts, 2048 -> 768: 163 us against 91 us
-// for its bytes at the rate of a copy; their weights' gradients 212 us, 91 likewise (402 MB of
-// outputs, whose stores overlap little with the products); 8192 rows over 8 experts, two terms,
-// 12288 -> 4096: 1750 us, 944 TFLOP/s, of which 1390 with equal experts: a quarter is what
-// uneven experts leave idle in the last round.
+// Measured, BF16, calls among others on several cards: 8192^3 NT / NN / TN 886-901 / 845-890 /
+// 950-990 us (1220-1300 TFLOP/s, TN 1110-1160; a library's plain product 750).  32768 rows over
+// 128 experts, 2048 -> 768: 161-170 us (under a profiler, median 190) against 91 for its bytes at
+// the rate of a copy; their weights' gradients 206-217 (220), 91 likewise (402 MB of outputs,
+// whose stores overlap little with the products); 8192 rows over 8 experts, two terms, 12288 ->
+// 4096: 1710-1790 us (1810), 920-960 TFLOP/s; 1390 with equal experts: the rest is what uneven ones
+// leave idle.  Tiles are dealt by their number, whatever their height: the heaviest workgroup of
+// these three has 1.1 to 1.35 times the mean.
 #include "dgf_device.hpp"
 #include "dgf_experts.hpp"
 #include "dgf_rows.hpp"
@@ -119,10 +122,17 @@ __device__ __forceinline__ void zero_tail(uint16_t *tile, int rows, int kv) {
 }
 
 // The rows [lo, hi) of expert e, within the R there are whatever the offsets hold.
-// (Read as constants: by the scalar unit, beside the counted vector loads.)
+// (Read as constants: by the scalar unit, beside the counted vector loads.)  ALL: one expert has
+// all rows, without offsets.
+template <bool ALL>
 __device__ __forceinline__ void expert_rows(const GroupedParams &p, int e, int &lo, int &hi) {
+  if constexpr (ALL) {
+    lo = 0;
+    hi = (int)p.R;
+    return;
+  }
   const auto *off = (const __attribute__((address_space(4))) int *)(uintptr_t)p.off;
-  const int R = (int)p.R, l = off ? off[e] : 0, h = off ? off[e + 1] : R;
+  const int R = (int)p.R, l = off[e], h = off[e + 1];
   lo = l < 0 ? 0 : l > R ? R : l;
   hi = h < lo ? lo : h > R ? R : h;
 }
@@ -155,7 +165,7 @@ constexpr int kNoTile = -1;  // its e: there is none
 // by expert, summed up (every wave writes the same values), and the next 64 of them.
 constexpr int kTileCost = 8;
 
-template <int LAYOUT, int BM, int BN>
+template <int LAYOUT, int BM, int BN, bool ALL>
 struct Tiles {
   static constexpr bool TN = LAYOUT == DGF_LAYOUT_TN;
   static constexpr int HM = BM / 64, CW = BN / 64;
@@ -191,7 +201,7 @@ struct Tiles {
     if (lane == 0) sums[0] = 0;
     for (int e0 = 0; e0 < p.E; e0 += 64) {
       int l = 0, h = 0;
-      if (e0 + lane < p.E) expert_rows(p, e0 + lane, l, h);
+      if (e0 + lane < p.E) expert_rows<ALL>(p, e0 + lane, l, h);
       const bool in = e0 + lane < p.E;
       all += __shfl(wave_scan(in ? cost_of(h - l) : 0, lane), 63);
       const int t = wave_scan(in ? tiles_of(h - l) : 0, lane) + tiles;
@@ -206,7 +216,7 @@ struct Tiles {
     int64_t base = 0;
     for (int e0 = 0; e0 < p.E; e0 += 64) {
       int l = 0, h = 0;
-      if (e0 + lane < p.E) expert_rows(p, e0 + lane, l, h);
+      if (e0 + lane < p.E) expert_rows<ALL>(p, e0 + lane, l, h);
       const int64_t cost = e0 + lane < p.E ? cost_of(h - l) : 0, sum = wave_scan(cost, lane) + base;
       const uint64_t a = __ballot(sum > from), z = __ballot(sum > to);
       const int t = tiles_of(h - l);
@@ -251,7 +261,7 @@ struct Tiles {
         else past = mid;
       }
       int lo, hi;
-      expert_rows(p, e, lo, hi);
+      expert_rows<ALL>(p, e, lo, hi);
       const int units = (hi - lo + 63) / 64, rows = TN ? p.tiles_m : (units + HM - 1) / HM;
       const int c = at - sums[e];
       // (offsets that are not ascending can make the sums wrap: no tile then)
@@ -278,7 +288,8 @@ struct Tiles {
 
 // A workgroup's tiles as one stream of stages: while a stage is multiplied, the loads of
 // the next ones, of this tile or the ones after it, are under way.
-// OUT32: the sums are stored as they are, in FP32 (C, of any alignment, is of floats).
+// OUT32: the sums are stored as they are, in FP32 (C, of any alignment, is of floats), and one
+// expert has all rows.
 template <class T, int LAYOUT, int WN, int FMAX, int FNMAX, int NS, bool OUT32>
 struct Stream {
   static constexpr bool ATR = LAYOUT == DGF_LAYOUT_TN, BTR = LAYOUT != DGF_LAYOUT_NT;
@@ -295,7 +306,7 @@ struct Stream {
   int lane, wave, wm, wn;
   uint32_t lds0;
   // the loader: its tile, what is left of it and the addresses of the next stage's pieces
-  Tiles<LAYOUT, BM, BN> tiles;
+  Tiles<LAYOUT, BM, BN, OUT32> tiles;
   int ahead, next_number;  // its number in the run (kNoTile: no more), and the one to look at next
   int end;         // TN: its last sorted row, and 1
   int left, term;  // contraction elements left of the term
@@ -645,7 +656,7 @@ hipError_t grouped_launch(GroupedParams p, int groups, hipStream_t s) {
   constexpr int BM = 32 * FM, BN = 16 * WN * FN;
   p.tiles_m = (p.M + BM - 1) / BM;
   p.tiles_n = (p.N + BN - 1) / BN;
-  dgf_launch((k_grouped<T, LAYOUT, WN, FM, FN, NS, OUT32>), dim3(groups), dim3(128 * WN), (size_t)NS * (BM + BN) * kU * 2 + Tiles<LAYOUT, BM, BN>::bytes(p.E), s, p);
+  dgf_launch((k_grouped<T, LAYOUT, WN, FM, FN, NS, OUT32>), dim3(groups), dim3(128 * WN), (size_t)NS * (BM + BN) * kU * 2 + Tiles<LAYOUT, BM, BN, OUT32>::bytes(p.E), s, p);
   return hipGetLastError();
 }
 
