@@ -7,11 +7,11 @@
 // to the same workgroups, adds up those of all of them, and every pair's row follows from its
 // expert's first, the earlier workgroups', waves' and lanes' pairs: a stable sort without
 // another pass over anything.  The bound is the two launches and the chain of k reductions,
-// not the 2.6 MB it moves: 5.4 and 6.4 us for 4096 tokens, 8 of 128 experts.  Up to 64 tokens
+// not the 2.6 MB it moves: 5.8 and 6.9 us for 4096 tokens, 8 of 128 experts.  Up to 64 tokens
 // one workgroup does both.
 // Combination: k rows of H gathered to one, 8 columns a thread, all rows under way at once:
-// bound by HBM (4096 x 2048, 8 rows each: 29.7 us, 5.1 TB/s; backward, with the k dot
-// products of a token kept in registers and reduced once, 53.6 us, 5.3 TB/s).
+// bound by HBM (4096 x 2048, 8 rows each: 29.5 us, 5.1 TB/s; backward, with the k dot
+// products of a token kept in registers and reduced once, 53.3 us, 5.3 TB/s).
 #include "dgf_experts.hpp"
 #include "dgf_rows.hpp"
 

@@ -11,11 +11,11 @@
 // The activations pass from gate/up to down in three BF16 parts, which add up to the FP32 value:
 // 30 of 131072 outputs then round otherwise than the exact sum does, against 180 of a product
 // in FP32 and 330 with two parts, 17 bits (12288 activations, 32 tokens).
-// Measured at 4096 x 12288, groups of 64, BF16, medians: gate/up 14.0 us for one token (53 MB,
-// 3.8 TB/s), 19.6 for 32; down 12.4 and 27.5.  What is left over the copy rate (10 and 5 us) is one
+// Measured at 4096 x 12288, groups of 64, BF16, medians: gate/up 13.0 us for one token (53 MB,
+// 4.1 TB/s), 18.8 for 32; down 12.8 and 26.4.  What is left over the copy rate (10 and 5 us) is one
 // start-up of loads and one reduction a workgroup, and past 16 tokens the activations: each of the
 // down product's 256 workgroups reads all 2.4 MB of them from L2, 600 MB (two parts: 20.8 us; two
-// row tiles a workgroup, on half the CUs: 32).
+// row tiles a workgroup, on half the CUs: 31).
 #include "dgf_experts.hpp"
 #include "dgf_rows.hpp"
 
@@ -196,11 +196,11 @@ template <class X, class S, int MT, int NT, int XP, bool PAIR, int GS, bool TAIL
 __global__ __launch_bounds__(64 * kW4Waves) void k_w4(W4Params p) {
   constexpr int W = PAIR ? 2 : 1;
   // Tiles in a ring of registers: each is loaded anew as soon as it has been used, so that all
-  // but one are on their way.  At 4096 x 12288 against activations one tile ahead and codes two
-  // or four: gate/up 12.4 us against 14.4 for one token and 16.4 against 23.1 for 32.  (Gate/up,
-  // one token, 4: 15.5 us, fewer waves fit.  TAIL's loads take more registers, and activations in
-  // parts too: the whole FFN takes 24.3 us with two tiles of down in flight, 25.3 with four, and at
-  // 32 tokens 42.3 with one, 42.2 with two.)
+  // but one are on their way.  At 4096 x 12288 (codes then took two operations a pair) against
+  // activations one tile ahead and codes two or four: gate/up 12.4 us against 14.4 for one token
+  // and 16.4 against 23.1 for 32.  (Gate/up, one token, 4: 15.5 us, fewer waves fit.  TAIL's loads
+  // take more registers, and activations in parts too: the whole FFN takes 24.3 us with two
+  // tiles of down in flight, 25.3 with four, and at 32 tokens 42.3 with one, 42.2 with two.)
   constexpr int R = XP > 1 ? (MT > 1 ? 1 : 2) : MT > 1 ? (TAIL ? 1 : 2) : PAIR || TAIL ? 2 : 4;
   extern __shared__ __attribute__((aligned(16))) float red[];  // [waves][W NT MT][4][64]
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
